@@ -317,6 +317,160 @@ RET_API int ret_chunkwise_backward(const void* q, const void* k, const void* v,
 RET_API int ret_rotate(const void* x, void* y, const float* theta, long long pos0, int B, int H,
                int N, int d, int dtype, void* stream);
 
+/*
+ * Gated linear recurrence: the recurrent form above ("RetNet - Retentive
+ * Network - A Successor to Transformer for LLMs", Key Equations, Recurrent
+ * Form) with a decay computed from the input, one per channel and token, and
+ * one state value per channel (the layers that a decoder mixes with
+ * retention; the pages give no such layer):
+ *     RET_SCAN_LOGIT   a = sigmoid(f),  h_t = a_t h_(t-1) + (1 - a_t) x_t
+ *     RET_SCAN_LOG     a = exp(f),      h_t = a_t h_(t-1) + x_t
+ * y_t = h_t, or swish(gate_t) h_t when a gate is given.  f = -inf is a decay
+ * of 0: nothing of the state before that token counts (a document that starts
+ * inside a packed row).  RET_SCAN_LOG expects f <= 0; larger values grow.
+ *   x, f, gate : [B][N][D] of type dtype; gate may be NULL.
+ *   y          : [B][N][D] of type dtype.
+ *   pitches    : HOST array {x, f, gate, y} x {batch, token}: elements from
+ *                one batch row, and from one token, to the next; NULL: all
+ *                dense.  Operands may so be slices of one projection's output,
+ *                a span of a longer sequence, or time-major ([N][B][D]); rows
+ *                of one operand must not share elements.  The gate's two are
+ *                not used without a gate.
+ *   state_in   : [B][D] float32 entering the first token; NULL means zero.
+ *   state_out  : [B][D] float32 after the last token; NULL: not written.  May
+ *                equal state_in.
+ *   chunk_states : [B][ceil(N / RET_SCAN_CHUNK)][D] float32, the state
+ *                entering every RET_SCAN_CHUNK-th token, which
+ *                ret_scan_backward needs; NULL: not written.
+ *   workspace  : at least ret_scan_workspace() bytes, 16-byte aligned;
+ *                contents on entry do not matter.  Calls that may overlap on
+ *                the GPU need a workspace each.
+ * The recurrence runs in float32 whatever dtype is, with 1 - a taken directly
+ * (decays near 1 keep their precision); y is rounded once.  The result does
+ * not depend on timing: the same call gives the same bits.
+ * Supported: B, D >= 1, N >= 0 (N == 0 copies or zeroes state_out and writes
+ * nothing else), any D; x, f, gate and y need the alignment of their element
+ * type only, and run fastest where pointers and pitches are multiples of 16
+ * bytes.
+ * Outputs must not overlap inputs or one another (state_out == state_in and
+ * interleaved slices of one buffer apart): RET_EINVAL.
+ */
+#define RET_SCAN_CHUNK 64
+typedef enum { RET_SCAN_LOGIT = 0, RET_SCAN_LOG = 1 } ret_scan_form;
+
+RET_API size_t ret_scan_workspace(int B, int N, int D, int dtype);
+RET_API int ret_scan(const void* x, const void* f, const void* gate, const float* state_in,
+                     float* state_out, float* chunk_states, void* y, const long long* pitches,
+                     int B, int N, int D, int form, int dtype, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/*
+ * One token of the recurrence for every batch row: x, f, gate and y are [B]
+ * rows of D elements; the state [B][D] float32 is read from state_in and
+ * written to state_out, which may be the same array.
+ *   pitches : HOST array {x, f, gate, y}: elements from one batch row to the
+ *             next; NULL: dense.
+ */
+RET_API int ret_scan_step(const void* x, const void* f, const void* gate, const float* state_in,
+                          float* state_out, void* y, const long long* pitches, int B, int D,
+                          int form, int dtype, void* stream);
+
+/*
+ * Backward of ret_scan: with d_y the gradient of y and d_state_out that of the
+ * final state (NULL: zero), writes the gradients of x, f, the gate and the
+ * initial state.
+ *   x, f, gate, chunk_states : as in, and from, the forward call.
+ *   grad_x, grad_f, grad_gate : [B][N][D] of type dtype; grad_gate is required
+ *                with a gate and not used without one.
+ *   d_state_in : [B][D] float32, or NULL.  May equal d_state_out.
+ *   pitches    : HOST array {x, f, gate, d_y, grad_x, grad_f, grad_gate} x
+ *                {batch, token}; NULL: all dense.
+ *   workspace  : at least ret_scan_workspace() bytes, as for ret_scan.
+ * Where a decay is 0 (f = -inf) the gradient of f is 0.  Other rules as for
+ * ret_scan; N == 0 copies or zeroes d_state_in.
+ */
+RET_API int ret_scan_backward(const void* x, const void* f, const void* gate,
+                              const float* chunk_states, const void* d_y,
+                              const float* d_state_out, void* grad_x, void* grad_f,
+                              void* grad_gate, float* d_state_in, const long long* pitches, int B,
+                              int N, int D, int form, int dtype, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * Norm and output gate of retention as a pass of their own ("RetNet -
+ * Retentive Network - A Successor to Transformer for LLMs", core components,
+ * item 4): o = swish(gate) (.) z with z each row of d_v outputs normalised,
+ *     RET_NORM_LAYER   z = (y - mean) / sqrt(var + eps)   (the GroupNorm of
+ *                      the gn_eps argument above: biased, no affine)
+ *     RET_NORM_RMS     z = y / sqrt(mean(y^2) + eps).
+ * The fused forward calls (ret_chunkwise_gated ...) do not keep y; training
+ * runs ret_chunkwise, then this, and its backward before
+ * ret_chunkwise_backward.
+ *   y    : [B][H][N][dv], as retention writes it.
+ *   gate, o : [B][H][N][dv] when token_major is 0, else [B][N][H][dv] with ldg
+ *          and ldo elements from one token to the next (0: H dv, dense; at
+ *          least H dv and a multiple of 8 otherwise), so that the gate may be
+ *          a slice of a projection and o feeds the next one.  gate may be
+ *          NULL (norm only).  o may equal y or gate where their layouts and
+ *          pitches agree; outputs must not overlap inputs otherwise.
+ * Supported: dv a multiple of 8 in [8, 1024]; all pointers 16-byte aligned;
+ * N == 0 writes nothing.
+ *
+ * Backward: with d_o the gradient of o (laid out like o, pitch lddo), writes
+ * grad_y ([B][H][N][dv]) and, with a gate, grad_gate (laid out like gate,
+ * pitch ldgg).  grad_y may equal y, grad_gate may equal gate or d_o.
+ */
+typedef enum { RET_NORM_NONE = -1, RET_NORM_LAYER = 0, RET_NORM_RMS = 1 } ret_norm_kind;
+
+RET_API int ret_norm_gate(const void* y, const void* gate, void* o, int B, int H, int N, int dv,
+                          int norm, float eps, int token_major, long long ldg, long long ldo,
+                          int dtype, void* stream);
+RET_API int ret_norm_gate_backward(const void* y, const void* gate, const void* d_o, void* grad_y,
+                                   void* grad_gate, int B, int H, int N, int dv, int norm,
+                                   float eps, int token_major, long long ldg, long long lddo,
+                                   long long ldgg, int dtype, void* stream);
+
+/*
+ * Residual sum with the norms around it ("RetNet - Retentive Network - A
+ * Successor to Transformer for LLMs", framework graph: norm and residual of
+ * the block), one pass:
+ *     u        = w_post (.) N_post(x)
+ *     res_out  = alpha residual + beta u
+ *     y        = w (.) N(res_out)
+ * N is a norm over the d features of a row as for ret_norm_gate; post_norm
+ * may be RET_NORM_NONE (then u = w_post (.) x, a scale per channel).
+ *   x, residual, res_out, y : [rows][d] of type dtype; residual may be NULL
+ *              (zero).  res_out may equal residual or x, y may equal x or
+ *              residual; no other overlap.
+ *   w, w_post : [d] float32, NULL means ones.
+ * The sum is kept in float32 for y and rounded once into res_out.
+ * Supported: d in [1, 16384], rows >= 0; elements of x, residual, res_out and
+ * y aligned to their type (fastest with 16-byte aligned rows); w and w_post
+ * 16-byte aligned.
+ *
+ * Backward: from res_out (as stored), x, and the gradients d_y of y and
+ * d_res_out of res_out (NULL: zero), writes
+ *   grad_x, grad_residual : [rows][d] of type dtype, each may be NULL
+ *   grad_w, grad_w_post   : [d] float32, each may be NULL (rows == 0: zeroed);
+ *              the same bits every time
+ *   x         : read only where post_norm is a norm or grad_w_post is given
+ *              (may be NULL otherwise).
+ *   workspace : at least ret_add_norm_backward_workspace() bytes when grad_w
+ *              or grad_w_post is given, 16-byte aligned.
+ * No output may overlap an input, except that grad_residual and grad_x may
+ * each equal d_y, d_res_out, res_out or x (not both the same array).
+ */
+RET_API int ret_add_norm(const void* x, const void* residual, const float* w_post, const float* w,
+                         void* res_out, void* y, long long rows, int d, int post_norm, int norm,
+                         float alpha, float beta, float eps, int dtype, void* stream);
+RET_API size_t ret_add_norm_backward_workspace(long long rows, int d);
+RET_API int ret_add_norm_backward(const void* x, const void* res_out, const float* w_post,
+                                  const float* w, const void* d_y, const void* d_res_out,
+                                  void* grad_x, void* grad_residual, float* grad_w,
+                                  float* grad_w_post, long long rows, int d, int post_norm,
+                                  int norm, float alpha, float beta, float eps, int dtype,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
 /* Human-readable name of a ret_status value (static storage). */
 RET_API const char* ret_status_string(int status);
 

@@ -19,9 +19,13 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libretentio
 
 RET_F32, RET_BF16 = 0, 1
 RET_OK, RET_EINVAL, RET_EUNSUPPORTED, RET_ECUDA, RET_EWORKSPACE = 0, -1, -2, -3, -4
+SCAN_CHUNK = 64                                    # RET_SCAN_CHUNK
+SCAN_FORMS = {"logit": 0, "log": 1}                # ret_scan_form
+NORMS = {None: -1, "layer": 0, "rms": 1}           # ret_norm_kind
 
 # name -> (restype, argtypes) of every symbol include/retention.h declares
 _P, _I, _F, _S = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_L = ctypes.c_longlong
 SIGNATURES = {
     "ret_parallel": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P]),
     "ret_chunkwise_workspace": (_S, [_I, _I, _I, _I, _I, _I, _I]),
@@ -45,6 +49,18 @@ SIGNATURES = {
     "ret_chunkwise_backward": (_I, [_P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I,
                                     _I, _I, _I, _P, _S, _P]),
     "ret_rotate": (_I, [_P, _P, _P, ctypes.c_longlong, _I, _I, _I, _I, _I, _P]),
+    "ret_scan_workspace": (_S, [_I, _I, _I, _I]),
+    "ret_scan": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _S, _P]),
+    "ret_scan_step": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
+    "ret_scan_backward": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P,
+                               _S, _P]),
+    "ret_norm_gate": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _L, _L, _I, _P]),
+    "ret_norm_gate_backward": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _L, _L, _L,
+                                    _I, _P]),
+    "ret_add_norm": (_I, [_P, _P, _P, _P, _P, _P, _L, _I, _I, _I, _F, _F, _F, _I, _P]),
+    "ret_add_norm_backward_workspace": (_S, [_L, _I]),
+    "ret_add_norm_backward": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _L, _I, _I, _I, _F, _F,
+                                   _F, _I, _P, _S, _P]),
     "ret_status_string": (ctypes.c_char_p, [_I]),
     "ret_last_cuda_error": (_I, []),
     "ret_version": (ctypes.c_char_p, []),
@@ -399,3 +415,321 @@ def step(q, k, v, gammas, state, gn_eps=None, out=None, gate=None, theta=None, p
     if s != RET_OK:
         _raise("ret_step", s)
     return out
+
+
+def _code(names, name, what):
+    try:
+        return names[name]
+    except (KeyError, TypeError):
+        raise ValueError(f"unknown {what} {name!r}; use one of {list(names)}") from None
+
+
+def _same(t, name, dtype, shape, device):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _pitches(shape, dtype, device, **operands):
+    """Pitches (elements) of the [..., D] operands, in order: a host array for
+    the library with one entry per leading axis of each, or None when all are
+    dense.  Channels must be adjacent; the library checks the rest."""
+    strided = False
+    for name, t in operands.items():
+        if t is not None:
+            _same(t, name, dtype, shape, device)
+            strided = strided or not t.is_contiguous()
+    if not strided:
+        return None
+    lead = len(shape) - 1
+    got = []
+    for name, t in operands.items():
+        if t is None:
+            got += [0] * lead
+            continue
+        st = t.stride()
+        if shape[-1] > 1 and st[-1] != 1:
+            raise ValueError(f"{name}: channels must be adjacent, got strides {st}")
+        got += st[:-1]
+    return (_L * len(got))(*got)
+
+
+def _call(name, device, *args):
+    """Runs a library call on the current stream of `device`, with that device
+    current; raises on a status other than RET_OK."""
+    torch = _torch()
+    lib = load_library()
+    if device.index == torch.cuda.current_device():
+        s = getattr(lib, name)(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            s = getattr(lib, name)(*args, torch.cuda.current_stream(device).cuda_stream)
+    if s != RET_OK:
+        _raise(name, s)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _own_workspace(workspace, need, device):
+    torch = _torch()
+    if workspace is None:
+        if need == 0:
+            return None, 0
+        return torch.empty(need, dtype=torch.uint8, device=device), need
+    _check(workspace, "workspace", device=device)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _state(t, name, shape, device):
+    if t is not None:
+        _check(t, name, dtype=_torch().float32, shape=shape, device=device)
+
+
+def scan_workspace_bytes(B, N, D, dtype) -> int:
+    code = RET_BF16 if dtype == _torch().bfloat16 else RET_F32
+    return int(load_library().ret_scan_workspace(B, N, D, code))
+
+
+def scan(x, f, form="logit", gate=None, state_in=None, state_out=None, return_state=False,
+         chunk_states=None, return_chunk_states=False, out=None, workspace=None):
+    """Gated linear recurrence over [B,N,D] (ret_scan): h_t = a_t h_(t-1) + u_t
+    per channel, with a = sigmoid(f), u = (1 - a) x (form "logit") or
+    a = exp(f), u = x (form "log"); returns y = h, or swish(gate) * h.
+
+    x, f, gate and out: [B,N,D] of one dtype (gate may be None), dense, slices
+    of a projection's output, a span of a longer sequence, or a time-major
+    tensor seen as [B,N,D]; channels must be adjacent.
+    state_in, state_out: [B,D] float32 before the first and after the last
+    token; state_out may be state_in.  chunk_states:
+    [B, ceil(N / SCAN_CHUNK), D] float32, kept for scan_backward.
+    Returns y, or the tuple (y[, state][, chunk_states]) with what
+    return_state / state_out and return_chunk_states / chunk_states ask for.
+    """
+    torch = _torch()
+    if x.dim() != 3:
+        raise ValueError("x must be [B,N,D]")
+    shape, dev, dt = x.shape, x.device, x.dtype
+    code, kind = _dtype_code(x), _code(SCAN_FORMS, form, "form")
+    B, N, D = shape
+    _state(state_in, "state_in", (B, D), dev)
+    if state_out is None and return_state:
+        state_out = torch.empty((B, D), dtype=torch.float32, device=dev)
+    else:
+        _state(state_out, "state_out", (B, D), dev)
+    if chunk_states is None and return_chunk_states:
+        chunk_states = torch.empty((B, -(-N // SCAN_CHUNK), D), dtype=torch.float32, device=dev)
+    else:
+        _state(chunk_states, "chunk_states", (B, -(-N // SCAN_CHUNK), D), dev)
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=dev)
+    pitches = _pitches(shape, dt, dev, x=x, f=f, gate=gate, out=out)
+    workspace, wsb = _own_workspace(workspace, load_library().ret_scan_workspace(B, N, D, code),
+                                    dev)
+    _call("ret_scan", dev, _addr(x), _addr(f), _addr(gate), _addr(state_in), _addr(state_out),
+          _addr(chunk_states), _addr(out), pitches, B, N, D, kind, code, _addr(workspace), wsb)
+    got = tuple(t for t in (state_out, chunk_states) if t is not None)
+    return (out,) + got if got else out
+
+
+def scan_step(x, f, state, form="logit", gate=None, out=None, state_out=None):
+    """One token of the gated linear recurrence (ret_scan_step): x, f, gate
+    [B,D]; state [B,D] float32 is updated in place, or left alone with the new
+    state written to state_out.  Returns y."""
+    torch = _torch()
+    if x.dim() != 2:
+        raise ValueError("x must be [B,D] for a single token")
+    shape, dev, dt = x.shape, x.device, x.dtype
+    code, kind = _dtype_code(x), _code(SCAN_FORMS, form, "form")
+    B, D = shape
+    _state(state, "state", shape, dev)
+    _state(state_out, "state_out", shape, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=dev)
+    pitches = _pitches(shape, dt, dev, x=x, f=f, gate=gate, out=out)
+    _call("ret_scan_step", dev, _addr(x), _addr(f), _addr(gate), _addr(state),
+          _addr(state if state_out is None else state_out), _addr(out), pitches, B, D, kind, code)
+    return out
+
+
+def scan_backward(x, f, chunk_states, d_y, form="logit", gate=None, d_state_out=None,
+                  grad_x=None, grad_f=None, grad_gate=None, workspace=None):
+    """Backward of scan (ret_scan_backward): returns (grad_x, grad_f, grad_gate
+    or None, d_state_in) for the gradient d_y of y and, optionally, d_state_out
+    of the final state.  chunk_states comes from the forward call with the same
+    x, f and state_in.  grad_x, grad_f and grad_gate may be given as slices of
+    one buffer."""
+    torch = _torch()
+    if x.dim() != 3:
+        raise ValueError("x must be [B,N,D]")
+    shape, dev, dt = x.shape, x.device, x.dtype
+    code, kind = _dtype_code(x), _code(SCAN_FORMS, form, "form")
+    B, N, D = shape
+    _state(chunk_states, "chunk_states", (B, -(-N // SCAN_CHUNK), D), dev)
+    _state(d_state_out, "d_state_out", (B, D), dev)
+    if gate is None and grad_gate is not None:
+        raise ValueError("grad_gate given without a gate")
+    grad_x = torch.empty(shape, dtype=dt, device=dev) if grad_x is None else grad_x
+    grad_f = torch.empty(shape, dtype=dt, device=dev) if grad_f is None else grad_f
+    if gate is not None and grad_gate is None:
+        grad_gate = torch.empty(shape, dtype=dt, device=dev)
+    pitches = _pitches(shape, dt, dev, x=x, f=f, gate=gate, d_y=d_y, grad_x=grad_x, grad_f=grad_f,
+                       grad_gate=grad_gate)
+    d_state_in = torch.empty((B, D), dtype=torch.float32, device=dev)
+    workspace, wsb = _own_workspace(workspace, load_library().ret_scan_workspace(B, N, D, code),
+                                    dev)
+    _call("ret_scan_backward", dev, _addr(x), _addr(f), _addr(gate), _addr(chunk_states),
+          _addr(d_y), _addr(d_state_out), _addr(grad_x), _addr(grad_f), _addr(grad_gate),
+          _addr(d_state_in), pitches, B, N, D, kind, code, _addr(workspace), wsb)
+    return grad_x, grad_f, grad_gate, d_state_in
+
+
+def _head_args(y, token_major):
+    if y.dim() != 4:
+        raise ValueError("y must be [B,H,N,dv]")
+    _check(y, "y")
+    B, H, N, dv = y.shape
+    return B, H, N, dv, (B, N, H, dv) if token_major else (B, H, N, dv)
+
+
+def _head_pitch(t, name, dt, shape, dev, token_major):
+    """Elements between tokens of a [B,N,H,dv] tensor whose heads are adjacent and
+    whose tokens are evenly spaced (0 for the head-major layout, which must be
+    dense)."""
+    if not token_major:
+        _check(t, name, dtype=dt, shape=shape, device=dev)
+        return 0
+    _same(t, name, dt, shape, dev)
+    if t.is_contiguous():
+        return 0
+    B, N, H, dv = shape
+    sb, sn, sh, sd = t.stride()
+    ld = sn if N > 1 else (sb if B > 1 else H * dv)
+    if sd != 1 or (H > 1 and sh != dv) or (B > 1 and N > 1 and sb != N * sn):
+        raise ValueError(f"{name}: heads must be adjacent and tokens evenly spaced, "
+                         f"got strides {t.stride()}")
+    return ld
+
+
+def norm_gate(y, gate=None, norm="layer", eps=1e-5, token_major=False, out=None):
+    """Per-head norm and output gate of retention outputs (ret_norm_gate):
+    o = swish(gate) * z, z each row of y [B,H,N,dv] normalised ("layer": the
+    GroupNorm of gn_eps; "rms").  With token_major, gate and o are [B,N,H,dv]
+    (dense, or the gate a slice of a projection's output viewed as such);
+    otherwise [B,H,N,dv].  gate None: o = z.  Returns o."""
+    torch = _torch()
+    B, H, N, dv, shape = _head_args(y, token_major)
+    dev, dt, code = y.device, y.dtype, _dtype_code(y)
+    kind = _code({"layer": 0, "rms": 1}, norm, "norm")
+    ldg = 0 if gate is None else _head_pitch(gate, "gate", dt, shape, dev, token_major)
+    if out is None:
+        out, ldo = torch.empty(shape, dtype=dt, device=dev), 0
+    else:
+        ldo = _head_pitch(out, "out", dt, shape, dev, token_major)
+    _call("ret_norm_gate", dev, _addr(y), _addr(gate), _addr(out), B, H, N, dv, kind, float(eps),
+          int(token_major), ldg, ldo, code)
+    return out
+
+
+def norm_gate_backward(y, gate, d_o, norm="layer", eps=1e-5, token_major=False, grad_y=None,
+                       grad_gate=None):
+    """Backward of norm_gate (ret_norm_gate_backward): returns (grad_y,
+    grad_gate or None).  d_o and grad_gate are laid out like o and gate."""
+    torch = _torch()
+    B, H, N, dv, shape = _head_args(y, token_major)
+    dev, dt, code = y.device, y.dtype, _dtype_code(y)
+    kind = _code({"layer": 0, "rms": 1}, norm, "norm")
+    ldg = 0 if gate is None else _head_pitch(gate, "gate", dt, shape, dev, token_major)
+    lddo = _head_pitch(d_o, "d_o", dt, shape, dev, token_major)
+    if grad_y is None:
+        grad_y = torch.empty_like(y)
+    _check(grad_y, "grad_y", dtype=dt, shape=y.shape, device=dev)
+    ldgg = 0
+    if gate is None:
+        if grad_gate is not None:
+            raise ValueError("grad_gate given without a gate")
+    elif grad_gate is None:
+        grad_gate = torch.empty(shape, dtype=dt, device=dev)
+    else:
+        ldgg = _head_pitch(grad_gate, "grad_gate", dt, shape, dev, token_major)
+    _call("ret_norm_gate_backward", dev, _addr(y), _addr(gate), _addr(d_o), _addr(grad_y),
+          _addr(grad_gate), B, H, N, dv, kind, float(eps), int(token_major), ldg, lddo, ldgg, code)
+    return grad_y, grad_gate
+
+
+def _weight(w, name, d, dev):
+    if w is not None:
+        _check(w, name, dtype=_torch().float32, shape=(d,), device=dev)
+
+
+def add_norm(x, residual, w=None, w_post=None, post_norm=None, norm="rms", alpha=1.0, beta=1.0,
+             eps=1e-5, res_out=None, out=None):
+    """Residual sum with the norms around it (ret_add_norm), over the last
+    axis of x [..., d]: u = w_post * N_post(x), r = alpha * residual + beta * u,
+    y = w * N(r); returns (r, y).  norm and post_norm: "rms" or "layer"
+    (post_norm None: no norm); w, w_post: [d] float32 or None; residual may be
+    None.  res_out may be residual (in place)."""
+    torch = _torch()
+    dev, dt, code, shape = x.device, x.dtype, _dtype_code(x), x.shape
+    if x.dim() < 1:
+        raise ValueError("x must have a feature axis")
+    _check(x, "x")
+    d = shape[-1]
+    if residual is not None:
+        _check(residual, "residual", dtype=dt, shape=shape, device=dev)
+    _weight(w, "w", d, dev)
+    _weight(w_post, "w_post", d, dev)
+    if res_out is None:
+        res_out = torch.empty_like(x)
+    else:
+        _check(res_out, "res_out", dtype=dt, shape=shape, device=dev)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _check(out, "out", dtype=dt, shape=shape, device=dev)
+    _call("ret_add_norm", dev, _addr(x), _addr(residual), _addr(w_post), _addr(w), _addr(res_out),
+          _addr(out), x.numel() // d if d else 0, d, _code(NORMS, post_norm, "post_norm"),
+          _code({"layer": 0, "rms": 1}, norm, "norm"), float(alpha), float(beta), float(eps), code)
+    return res_out, out
+
+
+def add_norm_backward(x, res_out, w, d_y, d_res_out=None, w_post=None, post_norm=None, norm="rms",
+                      alpha=1.0, beta=1.0, eps=1e-5, grad_x=None, grad_residual=None,
+                      workspace=None):
+    """Backward of add_norm (ret_add_norm_backward) from the stored sum res_out:
+    returns (grad_x, grad_residual, grad_w or None, grad_w_post or None); a
+    weight that is None has no gradient.  x may be None where neither post_norm
+    nor w_post is given."""
+    torch = _torch()
+    dev, dt, code, shape = res_out.device, res_out.dtype, _dtype_code(res_out), res_out.shape
+    if res_out.dim() < 1:
+        raise ValueError("res_out must have a feature axis")
+    _check(res_out, "res_out")
+    d = shape[-1]
+    for t, name in ((x, "x"), (d_y, "d_y"), (d_res_out, "d_res_out"), (grad_x, "grad_x"),
+                    (grad_residual, "grad_residual")):
+        if t is not None:
+            _check(t, name, dtype=dt, shape=shape, device=dev)
+    _weight(w, "w", d, dev)
+    _weight(w_post, "w_post", d, dev)
+    grad_x = torch.empty_like(res_out) if grad_x is None else grad_x
+    grad_residual = torch.empty_like(res_out) if grad_residual is None else grad_residual
+    grad_w = None if w is None else torch.empty_like(w)
+    grad_w_post = None if w_post is None else torch.empty_like(w_post)
+    rows = res_out.numel() // d if d else 0
+    need = 0
+    if grad_w is not None or grad_w_post is not None:
+        need = load_library().ret_add_norm_backward_workspace(rows, d)
+    workspace, wsb = _own_workspace(workspace, need, dev)
+    _call("ret_add_norm_backward", dev, _addr(x), _addr(res_out), _addr(w_post), _addr(w),
+          _addr(d_y), _addr(d_res_out), _addr(grad_x), _addr(grad_residual), _addr(grad_w),
+          _addr(grad_w_post), rows, d, _code(NORMS, post_norm, "post_norm"),
+          _code({"layer": 0, "rms": 1}, norm, "norm"), float(alpha), float(beta), float(eps), code,
+          _addr(workspace), wsb)
+    return grad_x, grad_residual, grad_w, grad_w_post

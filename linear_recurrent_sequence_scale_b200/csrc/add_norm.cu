@@ -1,0 +1,357 @@
+// Residual sum with the norms around it, and its backward.
+//
+// One row is the d features of one token.  With N(v) = (v - mean) r,
+// r = 1 / sqrt(var + eps) (layer) or N(v) = v r, r = 1 / sqrt(mean(v^2) + eps)
+// (RMS), the forward computes
+//     u  = w_post (.) N_post(x)          norm after the block (optional)
+//     r' = alpha residual + beta u       the residual stream
+//     y  = w (.) N(r')                   norm before the next block
+// ("RetNet - Retentive Network - A Successor to Transformer for LLMs",
+// framework graph: norm and residual around each sub-layer), and the backward, with
+// h = N(r') and hx = N_post(x),
+//     dr' = r (w dy - [mean(w dy)] - h mean(w dy (.) h)) + d res_out
+//     d residual = alpha dr',   dw = sum over rows of dy (.) h
+//     du = beta dr',   dw_post = sum over rows of du (.) hx
+//     dx = rx (w_post du - [mean(w_post du)] - hx mean(w_post du (.) hx)),
+// dx = w_post du without the norm after the block ([] for layer norms only).
+//
+// Bound by HBM: x, the residual and both outputs cross it once.  A row stays
+// in the registers of TPR threads, and its sums go through warp shuffles and,
+// for rows longer than a warp's, shared memory.  y is computed from r' before
+// its rounding to the storage type, so y carries one rounding only; the
+// backward starts from the stored r'.
+#include "common.cuh"
+#include "kernels.h"
+#include "rowvec.cuh"
+
+namespace ret {
+namespace an {
+
+// Sums of a and b over the TPR threads of a row.  `slot` (two floats per
+// warp) may be used again once every thread has passed another sum's barrier.
+template <int TPR> __device__ __forceinline__ void row_sum2(float& a, float& b, float2* slot) {
+#pragma unroll
+  for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  if constexpr (TPR > 32) {
+    constexpr int W = TPR / 32;
+    if (threadIdx.x % 32 == 0) slot[threadIdx.x / 32] = make_float2(a, b);
+    __syncthreads();
+    a = 0.0f, b = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) a += slot[w].x, b += slot[w].y;
+  }
+}
+template <int TPR> __device__ __forceinline__ float row_sum(float a, float2* slot) {
+  float b = 0.0f;
+  row_sum2<TPR>(a, b, slot);
+  return a;
+}
+
+// Row geometry: CH accesses of V elements per thread and tensor.
+template <typename T, int V, int CH, int TPR> struct Geo {
+  using type = T;
+  static constexpr int kV = V, kCH = CH, kTPR = TPR;
+  static constexpr int kThreads = TPR < 128 ? 128 : TPR;  // several short rows per block
+  static constexpr int kRows = kThreads / TPR;
+  static_assert(TPR <= 32 || kThreads == TPR, "the block barrier serves one row");
+};
+
+template <typename G> struct Row {
+  static constexpr int V = G::kV, CH = G::kCH, TPR = G::kTPR;
+  using T = typename G::type;
+  float v[CH][V];
+  template <typename S>  // elements past d read as zero
+  __device__ __forceinline__ void load(const S* p, int lane, int nv) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i = c * TPR + lane;
+      if (i < nv) {
+        load_pack<S, V>(p + (long long)i * V, v[c]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[c][k] = 0.0f;
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* p, int lane, int nv) const {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i = c * TPR + lane;
+      if (i < nv) store_pack<T, V>(p + (long long)i * V, v[c]);
+    }
+  }
+  // v <- v (.) w
+  __device__ __forceinline__ void scale(const float* w, int lane, int nv) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i = c * TPR + lane;
+      if (i < nv) {
+        constexpr int P = V < 4 ? V : 4;
+#pragma unroll
+        for (int j = 0; j < V; j += P) {
+          float f[P];
+          load_pack<float, P>(w + (long long)i * V + j, f);
+#pragma unroll
+          for (int k = 0; k < P; ++k) v[c][j + k] *= f[k];
+        }
+      }
+    }
+  }
+  // v <- v + a (.) b for a row that exists (nv > 0)
+  __device__ __forceinline__ void add_product(const Row& a, const Row& b, int lane, int nv) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      if (c * TPR + lane < nv) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[c][k] = fmaf(a.v[c][k], b.v[c][k], v[c][k]);
+      }
+  }
+  // v <- N(v); returns r.  Elements past d stay zero.
+  __device__ __forceinline__ float normalise(int lane, int nv, bool layer, float eps, float inv_d,
+                                             float2* slots) {
+    if (layer) {
+      float s = 0.0f;
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int k = 0; k < V; ++k) s += v[c][k];
+      const float mean = row_sum<TPR>(s, slots) * inv_d;
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+        if (c * TPR + lane < nv) {
+#pragma unroll
+          for (int k = 0; k < V; ++k) v[c][k] -= mean;
+        }
+    }
+    float q = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int k = 0; k < V; ++k) q = fmaf(v[c][k], v[c][k], q);
+    const float r = rsqrtf(fmaf(row_sum<TPR>(q, slots + 32), inv_d, eps));
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[c][k] *= r;
+    return r;
+  }
+  // v <- r (v - [mean(v)] - h mean(v (.) h)), the norm's backward
+  __device__ __forceinline__ void norm_backward(const Row& h, float r, int lane, int nv, bool layer,
+                                                float inv_d, float2* slot) {
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        s1 += v[c][k];
+        s2 = fmaf(v[c][k], h.v[c][k], s2);
+      }
+    row_sum2<TPR>(s1, s2, slot);
+    s1 = layer ? s1 * inv_d : 0.0f;
+    s2 *= inv_d;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      if (c * TPR + lane < nv) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[c][k] = r * (v[c][k] - s1 - h.v[c][k] * s2);
+      }
+  }
+};
+
+template <typename G>
+__global__ void __launch_bounds__(G::kThreads)
+add_norm_rows(AddNormArgs a) {
+  using T = typename G::type;
+  __shared__ float2 slots[4 * 32];
+  const int lane = threadIdx.x % G::kTPR, nv = a.d / G::kV;
+  const long long n = (long long)blockIdx.x * G::kRows + threadIdx.x / G::kTPR;
+  const int take = n < a.rows ? nv : 0;  // threads past the last row only join the sums
+  const long long at = min(n, a.rows - 1) * a.d;
+  const float inv_d = 1.0f / a.d;
+  Row<G> u, s;
+  u.load(static_cast<const T*>(a.x) + at, lane, take);
+  if (a.residual) s.load(static_cast<const T*>(a.residual) + at, lane, take);
+  if (a.post_norm != RET_NORM_NONE)
+    u.normalise(lane, take, a.post_norm == RET_NORM_LAYER, a.eps, inv_d, slots);
+  if (a.w_post) u.scale(a.w_post, lane, take);
+#pragma unroll
+  for (int c = 0; c < G::kCH; ++c)
+#pragma unroll
+    for (int k = 0; k < G::kV; ++k)
+      u.v[c][k] = a.residual ? fmaf(a.alpha, s.v[c][k], a.beta * u.v[c][k]) : a.beta * u.v[c][k];
+  u.store(static_cast<T*>(a.res_out) + at, lane, take);
+  u.normalise(lane, take, a.norm == RET_NORM_LAYER, a.eps, inv_d, slots + 64);
+  if (a.w) u.scale(a.w, lane, take);
+  u.store(static_cast<T*>(a.y) + at, lane, take);
+}
+
+// Persistent over rows: each block sums its rows' weight gradients in
+// registers and leaves one partial row per weight in the workspace.
+template <typename G>
+__global__ void __launch_bounds__(G::kThreads)
+add_norm_rows_backward(AddNormArgs a, float* part_w, float* part_post) {
+  using T = typename G::type;
+  __shared__ float2 slots[6 * 32];
+  const int lane = threadIdx.x % G::kTPR, nv = a.d / G::kV;
+  const float inv_d = 1.0f / a.d;
+  const bool need_x = a.post_norm != RET_NORM_NONE || part_post;
+  Row<G> acc_w, acc_post;
+#pragma unroll
+  for (int c = 0; c < G::kCH; ++c)
+#pragma unroll
+    for (int k = 0; k < G::kV; ++k) acc_w.v[c][k] = acc_post.v[c][k] = 0.0f;
+  const long long groups = (a.rows + G::kRows - 1) / G::kRows;
+  for (long long g = blockIdx.x; g < groups; g += gridDim.x) {
+    const long long n = g * G::kRows + threadIdx.x / G::kTPR;
+    const int take = n < a.rows ? nv : 0;
+    const long long at = min(n, a.rows - 1) * a.d;
+    Row<G> h, d, s, x;
+    h.load(static_cast<const T*>(a.res_out) + at, lane, take);
+    d.load(static_cast<const T*>(a.d_y) + at, lane, take);
+    if (a.d_res_out) s.load(static_cast<const T*>(a.d_res_out) + at, lane, take);
+    if (need_x) x.load(static_cast<const T*>(a.x) + at, lane, take);
+    const float r = h.normalise(lane, take, a.norm == RET_NORM_LAYER, a.eps, inv_d, slots);
+    if (part_w) acc_w.add_product(d, h, lane, take);
+    if (a.w) d.scale(a.w, lane, take);
+    d.norm_backward(h, r, lane, take, a.norm == RET_NORM_LAYER, inv_d, slots + 64);
+    if (a.d_res_out) {
+#pragma unroll
+      for (int c = 0; c < G::kCH; ++c)
+#pragma unroll
+        for (int k = 0; k < G::kV; ++k) d.v[c][k] += s.v[c][k];
+    }
+    if (a.grad_residual) {
+#pragma unroll
+      for (int c = 0; c < G::kCH; ++c)
+#pragma unroll
+        for (int k = 0; k < G::kV; ++k) s.v[c][k] = a.alpha * d.v[c][k];
+      s.store(static_cast<T*>(a.grad_residual) + at, lane, take);
+    }
+#pragma unroll
+    for (int c = 0; c < G::kCH; ++c)
+#pragma unroll
+      for (int k = 0; k < G::kV; ++k) d.v[c][k] *= a.beta;
+    float rx = 1.0f;
+    if (a.post_norm != RET_NORM_NONE)
+      rx = x.normalise(lane, take, a.post_norm == RET_NORM_LAYER, a.eps, inv_d, slots + 96);
+    if (part_post) acc_post.add_product(d, x, lane, take);
+    if (a.grad_x) {
+      if (a.w_post) d.scale(a.w_post, lane, take);
+      if (a.post_norm != RET_NORM_NONE)
+        d.norm_backward(x, rx, lane, take, a.post_norm == RET_NORM_LAYER, inv_d, slots + 160);
+      d.store(static_cast<T*>(a.grad_x) + at, lane, take);
+    }
+  }
+  // one partial row per row group of the block
+  const long long part = ((long long)blockIdx.x * G::kRows + threadIdx.x / G::kTPR) * a.d;
+#pragma unroll
+  for (int c = 0; c < G::kCH; ++c) {
+    const int i = c * G::kTPR + lane;
+    if (i >= nv) continue;
+#pragma unroll
+    for (int k = 0; k < G::kV; ++k) {
+      if (part_w) part_w[part + (long long)i * G::kV + k] = acc_w.v[c][k];
+      if (part_post) part_post[part + (long long)i * G::kV + k] = acc_post.v[c][k];
+    }
+  }
+}
+
+// grad[c] = sum of the partial rows, in a fixed order: 8 warps take every
+// eighth row of 32 columns, then their sums are added in order.
+constexpr int kReduceWarps = 8;
+__global__ void __launch_bounds__(32 * kReduceWarps)
+sum_partials(const float* __restrict__ part_w, const float* __restrict__ part_post,
+             float* __restrict__ grad_w, float* __restrict__ grad_post, int parts, int d) {
+  __shared__ float s[kReduceWarps][32];
+  const float* part = blockIdx.y ? part_post : part_w;
+  float* grad = blockIdx.y ? grad_post : grad_w;
+  if (!part) return;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, col = blockIdx.x * 32 + lane;
+  float sum = 0.0f;
+  if (col < d)
+    for (int p = warp; p < parts; p += kReduceWarps) sum += part[(long long)p * d + col];
+  s[warp][lane] = sum;
+  __syncthreads();
+  if (warp == 0 && col < d) {
+    for (int w = 1; w < kReduceWarps; ++w) sum += s[w][lane];
+    grad[col] = sum;
+  }
+}
+
+// Whether every row of every tensor splits into 16-byte pieces.
+bool vectored(const AddNormArgs& a) {
+  const int es = a.dtype == RET_BF16 ? 2 : 4;
+  if ((long long)a.d * es % 16) return false;
+  for (const void* p : {a.x, a.residual, (const void*)a.res_out, (const void*)a.y, a.d_y,
+                        a.d_res_out, (const void*)a.grad_x, (const void*)a.grad_residual})
+    if (p && !aligned_to(p, 16)) return false;
+  return true;
+}
+
+template <typename T, int V, int CH, typename Fn> cudaError_t by_threads(int nv, Fn fn) {
+  if (nv <= 32 * CH) return fn(Geo<T, V, CH, 32>());
+  if (nv <= 128 * CH) return fn(Geo<T, V, CH, 128>());
+  if (nv <= 256 * CH) return fn(Geo<T, V, CH, 256>());
+  if (nv <= 512 * CH) return fn(Geo<T, V, CH, 512>());
+  return fn(Geo<T, V, CH, 1024>());
+}
+
+// Calls fn with the row geometry for these sizes; d <= 16384.
+template <typename Fn> cudaError_t by_geometry(const AddNormArgs& a, Fn fn) {
+  const bool bf16 = a.dtype == RET_BF16;
+  if (vectored(a)) {
+    if (bf16) return by_threads<__nv_bfloat16, 8, 2>(a.d / 8, fn);
+    return a.d <= 8192 ? by_threads<float, 4, 2>(a.d / 4, fn) : fn(Geo<float, 4, 4, 1024>());
+  }
+  if (bf16)
+    return a.d <= 8192 ? by_threads<__nv_bfloat16, 1, 8>(a.d, fn)
+                       : fn(Geo<__nv_bfloat16, 1, 16, 1024>());
+  return a.d <= 8192 ? by_threads<float, 1, 8>(a.d, fn) : fn(Geo<float, 1, 16, 1024>());
+}
+
+// Blocks of the backward.  A fixed count, so that the order of the weight
+// gradients' sums does not depend on the device.
+constexpr int kMaxBlocks = 592;  // four per SM
+
+}  // namespace an
+
+size_t add_norm_backward_workspace_bytes(long long rows, int d) {
+  // a block leaves one partial row per weight, or one for each of its four
+  // rows where rows are short enough for a warp (512 elements at most)
+  const long long per_block = d <= 512 ? 4 : 1;
+  const long long parts =
+      per_block * (rows < an::kMaxBlocks ? (rows > 0 ? rows : 0) : an::kMaxBlocks);
+  return sizeof(float) * 2 * (size_t)parts * d;
+}
+
+cudaError_t launch_add_norm(const AddNormArgs& a, cudaStream_t st) {
+  return an::by_geometry(a, [&](auto geo) {
+    using G = decltype(geo);
+    const unsigned grid = static_cast<unsigned>((a.rows + G::kRows - 1) / G::kRows);
+    an::add_norm_rows<G><<<grid, G::kThreads, 0, st>>>(a);
+    return cudaPeekAtLastError();
+  });
+}
+
+cudaError_t launch_add_norm_backward(const AddNormArgs& a, float* ws, cudaStream_t st) {
+  return an::by_geometry(a, [&](auto geo) {
+    using G = decltype(geo);
+    const long long groups = (a.rows + G::kRows - 1) / G::kRows;
+    const int grid = static_cast<int>(groups < an::kMaxBlocks ? groups : an::kMaxBlocks);
+    const int parts = grid * G::kRows;
+    float* part_w = a.grad_w ? ws : nullptr;
+    float* part_post =
+        a.grad_w_post ? ws + (a.grad_w ? (size_t)parts * a.d : (size_t)0) : nullptr;
+    an::add_norm_rows_backward<G><<<grid, G::kThreads, 0, st>>>(a, part_w, part_post);
+    cudaError_t e = cudaPeekAtLastError();
+    if (e != cudaSuccess || !(part_w || part_post)) return e;
+    an::sum_partials<<<dim3(cdiv(a.d, 32), 2), 32 * an::kReduceWarps, 0, st>>>(
+        part_w, part_post, a.grad_w, a.grad_w_post, parts, a.d);
+    return cudaPeekAtLastError();
+  });
+}
+
+}  // namespace ret

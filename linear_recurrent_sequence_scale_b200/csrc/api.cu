@@ -455,3 +455,384 @@ int ret_rotate(const void* x, void* y, const float* theta, long long pos0, int B
 }
 
 }  // extern "C"
+
+namespace {
+
+// A [batches][rows] lattice of `width`-byte pieces.
+struct Extent {
+  const void* p;
+  int64_t batches, batch, rows, row, width;
+};
+
+Extent flat(const void* p, int64_t bytes) { return {p, 1, bytes, 1, bytes, bytes}; }
+
+// Whether pieces of wa and wb bytes that repeat every `period` bytes, `off`
+// bytes from one to the other, leave each other alone.
+bool apart(int64_t off, int64_t period, int64_t wa, int64_t wb) {
+  if (period < 1) return false;
+  off %= period;
+  if (off < 0) off += period;
+  return off >= wa && period - off >= wb;
+}
+
+int64_t reach(const Extent& e) {
+  return (e.batches - 1) * e.batch + (e.rows - 1) * e.row + e.width;
+}
+
+// Whether two arrays share a byte.  Slices of one buffer interleave without
+// sharing: channels of each token, or spans of each batch row's tokens (equal
+// pitches).  Other lattices whose ranges meet count as sharing.
+bool overlap(const Extent& a, const Extent& b) {
+  if (!a.p || !b.p || a.width < 1 || b.width < 1) return false;
+  const intptr_t pa = reinterpret_cast<intptr_t>(a.p), pb = reinterpret_cast<intptr_t>(b.p);
+  if (pa + reach(a) <= pb || pb + reach(b) <= pa) return false;
+  const int64_t off = pb - pa;
+  const bool one = a.batches == 1 && b.batches == 1;
+  if (!one && (a.batches != b.batches || a.batch != b.batch)) return true;
+  const int64_t wa = (a.rows - 1) * a.row + a.width, wb = (b.rows - 1) * b.row + b.width;
+  if (!one && a.batch > 0 && apart(off, a.batch, wa, wb)) return false;
+  if (a.rows != b.rows || a.row != b.row || a.rows == 1) return true;
+  // every piece starts at a multiple of the smaller pitch, if that divides the larger
+  int64_t period = a.row;
+  if (!one) {
+    const int64_t large = a.batch > a.row ? a.batch : a.row;
+    period = a.batch > a.row ? a.row : a.batch;
+    if (period < 1 || large % period) return true;
+  }
+  return !apart(off, period, a.width, b.width);
+}
+
+bool same(const Extent& a, const Extent& b) {
+  return a.p == b.p && a.batches == b.batches && a.rows == b.rows && a.width == b.width &&
+         (a.batches == 1 || a.batch == b.batch) && (a.rows == 1 || a.row == b.row);
+}
+
+// The outputs against the inputs and one another; aliasing(o, i) says whether
+// output o may be the very array that input i is.
+template <typename May>
+bool clash(const Extent* out, int n_out, const Extent* in, int n_in, May may) {
+  for (int o = 0; o < n_out; ++o) {
+    for (int i = 0; i < n_in; ++i)
+      if (overlap(out[o], in[i]) && !(may(o, i) && same(out[o], in[i]))) return true;
+    for (int q = 0; q < o; ++q)
+      if (overlap(out[o], out[q])) return true;
+  }
+  return false;
+}
+
+bool aligned_elem(const void* p, int dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & (dtype == RET_BF16 ? 1u : 3u)) == 0;
+}
+
+int64_t elem_bytes(int dtype) { return dtype == RET_BF16 ? 2 : 4; }
+
+int check_scan(int B, int N, int D, int form, int dtype) {
+  if (B < 1 || N < 0 || D < 1 || !valid_dtype(dtype)) return RET_EINVAL;
+  if (form != RET_SCAN_LOGIT && form != RET_SCAN_LOG) return RET_EINVAL;
+  const int64_t channels = (int64_t)B * D;
+  if (channels > INT32_MAX) return RET_EUNSUPPORTED;
+  if (N > 0 && channels > ((int64_t)1 << 40) / N) return RET_EUNSUPPORTED;
+  return RET_OK;
+}
+
+// An operand of the recurrence.  Rows must not share elements: batch rows
+// follow one another (batch pitch past the last token's row) or lie between
+// two tokens (time-major).
+int check_operand(const ret::Operand& o, int B, int N, int D, int dtype) {
+  constexpr int64_t kMost = (int64_t)1 << 44;
+  if (!o.p || !aligned_elem(o.p, dtype)) return RET_EINVAL;
+  if ((N > 1 && o.token < D) || (B > 1 && o.batch < D)) return RET_EINVAL;
+  if ((N > 1 && o.token > kMost / N) || (B > 1 && o.batch > kMost / B)) return RET_EUNSUPPORTED;
+  if (B > 1 && N > 1 && o.batch < (N - 1) * o.token + D && o.token < (B - 1) * o.batch + D)
+    return RET_EINVAL;
+  return RET_OK;
+}
+
+// Operand k of a call: its pitches in elements from the host array, or dense.
+ret::Operand operand(const void* p, const long long* pitches, int k, int N, int D) {
+  ret::Operand o = {const_cast<void*>(p), (long long)N * D, D};
+  if (pitches) o.batch = pitches[2 * k], o.token = pitches[2 * k + 1];
+  return o;
+}
+
+Extent extent(const ret::Operand& o, int B, int N, int D, int dtype) {
+  const int64_t es = elem_bytes(dtype);
+  return {o.p, B, (B > 1 ? o.batch : 0) * es, N, (N > 1 ? o.token : 0) * es, D * es};
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The final state of an empty sequence is the initial one.
+int pass_state(const float* in, float* out, int64_t n, void* stream) {
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!out || in == out) return RET_OK;
+  const size_t bytes = sizeof(float) * (size_t)n;
+  return cuda_status(in ? cudaMemcpyAsync(out, in, bytes, cudaMemcpyDeviceToDevice, st)
+                        : cudaMemsetAsync(out, 0, bytes, st));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ret_scan_workspace(int B, int N, int D, int dtype) {
+  if (check_scan(B, N, D, RET_SCAN_LOGIT, dtype) != RET_OK || N == 0) return 0;
+  return ret::scan_workspace_bytes(B, N, D, dtype);
+}
+
+int ret_scan(const void* x, const void* f, const void* gate, const float* state_in,
+             float* state_out, float* chunk_states, void* y, const long long* pitches, int B,
+             int N, int D, int form, int dtype, void* workspace, size_t workspace_bytes,
+             void* stream) {
+  int s = check_scan(B, N, D, form, dtype);
+  if (s) return s;
+  if (!aligned4(state_in) || !aligned4(state_out) || !aligned4(chunk_states)) return RET_EINVAL;
+  const int64_t state_bytes = 4 * (int64_t)B * D;
+  const Extent si = flat(state_in, state_bytes), so = flat(state_out, state_bytes);
+  if (overlap(si, so) && !same(si, so)) return RET_EINVAL;
+  if (N == 0) return pass_state(state_in, state_out, (int64_t)B * D, stream);
+  ret::ScanArgs a = {};
+  a.x = operand(x, pitches, 0, N, D), a.f = operand(f, pitches, 1, N, D);
+  a.gate = operand(gate, pitches, 2, N, D), a.y = operand(y, pitches, 3, N, D);
+  for (const ret::Operand* o : {&a.x, &a.f, &a.gate, &a.y})
+    if ((o != &a.gate || gate) && (s = check_operand(*o, B, N, D, dtype))) return s;
+  const size_t need = ret_scan_workspace(B, N, D, dtype);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return RET_EWORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return RET_EINVAL;
+  const int64_t chunks = (N + RET_SCAN_CHUNK - 1) / RET_SCAN_CHUNK;
+  const Extent in[] = {extent(a.x, B, N, D, dtype), extent(a.f, B, N, D, dtype),
+                       extent(a.gate, B, N, D, dtype), si};
+  const Extent out[] = {extent(a.y, B, N, D, dtype), so,
+                        flat(chunk_states, state_bytes * chunks), flat(workspace, (int64_t)need)};
+  if (clash(out, 4, in, 4, [](int o, int i) { return o == 1 && i == 3; })) return RET_EINVAL;
+  a.state_in = state_in, a.state_out = state_out, a.chunk_states = chunk_states;
+  a.B = B, a.N = N, a.D = D, a.form = form, a.dtype = dtype, a.workspace = workspace;
+  return cuda_status(ret::launch_scan(a, static_cast<cudaStream_t>(stream)));
+}
+
+int ret_scan_step(const void* x, const void* f, const void* gate, const float* state_in,
+                  float* state_out, void* y, const long long* pitches, int B, int D, int form,
+                  int dtype, void* stream) {
+  int s = check_scan(B, 1, D, form, dtype);
+  if (s) return s;
+  ret::ScanArgs a = {};
+  a.x = {const_cast<void*>(x), pitches ? pitches[0] : D, D};
+  a.f = {const_cast<void*>(f), pitches ? pitches[1] : D, D};
+  a.gate = {const_cast<void*>(gate), pitches ? pitches[2] : D, D};
+  a.y = {y, pitches ? pitches[3] : D, D};
+  for (const ret::Operand* o : {&a.x, &a.f, &a.gate, &a.y})
+    if ((o != &a.gate || gate) && (s = check_operand(*o, B, 1, D, dtype))) return s;
+  if (!state_in || !state_out || !aligned4(state_in) || !aligned4(state_out)) return RET_EINVAL;
+  const int64_t state_bytes = 4 * (int64_t)B * D;
+  const Extent in[] = {extent(a.x, B, 1, D, dtype), extent(a.f, B, 1, D, dtype),
+                       extent(a.gate, B, 1, D, dtype), flat(state_in, state_bytes)};
+  const Extent out[] = {extent(a.y, B, 1, D, dtype), flat(state_out, state_bytes)};
+  if (clash(out, 2, in, 4, [](int o, int i) { return o == 1 && i == 3; })) return RET_EINVAL;
+  a.state_in = state_in, a.state_out = state_out;
+  a.B = B, a.N = 1, a.D = D, a.form = form, a.dtype = dtype;
+  return cuda_status(ret::launch_scan_step(a, static_cast<cudaStream_t>(stream)));
+}
+
+int ret_scan_backward(const void* x, const void* f, const void* gate, const float* chunk_states,
+                      const void* d_y, const float* d_state_out, void* grad_x, void* grad_f,
+                      void* grad_gate, float* d_state_in, const long long* pitches, int B, int N,
+                      int D, int form, int dtype, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  int s = check_scan(B, N, D, form, dtype);
+  if (s) return s;
+  if (!aligned4(chunk_states) || !aligned4(d_state_out) || !aligned4(d_state_in))
+    return RET_EINVAL;
+  const int64_t state_bytes = 4 * (int64_t)B * D;
+  const Extent si = flat(d_state_out, state_bytes), so = flat(d_state_in, state_bytes);
+  if (overlap(si, so) && !same(si, so)) return RET_EINVAL;
+  if (N == 0) return pass_state(d_state_out, d_state_in, (int64_t)B * D, stream);
+  if (!gate) grad_gate = nullptr;
+  ret::ScanArgs a = {};
+  a.x = operand(x, pitches, 0, N, D), a.f = operand(f, pitches, 1, N, D);
+  a.gate = operand(gate, pitches, 2, N, D), a.d_y = operand(d_y, pitches, 3, N, D);
+  a.grad_x = operand(grad_x, pitches, 4, N, D), a.grad_f = operand(grad_f, pitches, 5, N, D);
+  a.grad_gate = operand(grad_gate, pitches, 6, N, D);
+  for (const ret::Operand* o :
+       {&a.x, &a.f, &a.gate, &a.d_y, &a.grad_x, &a.grad_f, &a.grad_gate})
+    if (((o != &a.gate && o != &a.grad_gate) || gate) &&
+        (s = check_operand(*o, B, N, D, dtype)))
+      return s;
+  if (!chunk_states) return RET_EINVAL;
+  const size_t need = ret_scan_workspace(B, N, D, dtype);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return RET_EWORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return RET_EINVAL;
+  const int64_t chunks = (N + RET_SCAN_CHUNK - 1) / RET_SCAN_CHUNK;
+  const Extent in[] = {extent(a.x, B, N, D, dtype), extent(a.f, B, N, D, dtype),
+                       extent(a.gate, B, N, D, dtype), extent(a.d_y, B, N, D, dtype),
+                       si, flat(chunk_states, state_bytes * chunks)};
+  const Extent out[] = {extent(a.grad_x, B, N, D, dtype), extent(a.grad_f, B, N, D, dtype),
+                        extent(a.grad_gate, B, N, D, dtype), so,
+                        flat(workspace, (int64_t)need)};
+  if (clash(out, 5, in, 6, [](int o, int i) { return o == 3 && i == 4; })) return RET_EINVAL;
+  a.chunk_states = const_cast<float*>(chunk_states);
+  a.d_state_out = d_state_out, a.d_state_in = d_state_in;
+  a.B = B, a.N = N, a.D = D, a.form = form, a.dtype = dtype, a.workspace = workspace;
+  return cuda_status(ret::launch_scan_backward(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+bool norm_kind(int norm) { return norm == RET_NORM_LAYER || norm == RET_NORM_RMS; }
+
+// Sizes of the norm-and-gate calls; a pitch of 0 becomes the dense one.
+int check_norm_gate(int B, int H, int N, int dv, int norm, float eps, int token_major, int dtype,
+                    long long** pitches, int n_pitches) {
+  if (B < 1 || H < 1 || N < 0 || dv < 8 || dv % 8 || !valid_dtype(dtype)) return RET_EINVAL;
+  if (!norm_kind(norm) || !(eps >= 0.0f) || isinf(eps)) return RET_EINVAL;
+  if (dv > 1024 || (int64_t)B * H > 65535) return RET_EUNSUPPORTED;
+  if ((int64_t)B * H * N * dv > ((int64_t)1 << 40)) return RET_EUNSUPPORTED;
+  const int64_t dense = (int64_t)H * dv;
+  for (int i = 0; i < n_pitches; ++i) {
+    if (!token_major || *pitches[i] == 0) *pitches[i] = dense;
+    if (*pitches[i] < dense || *pitches[i] % 8) return RET_EINVAL;
+    if (N > 0 && *pitches[i] > ((int64_t)1 << 44) / ((int64_t)B * N)) return RET_EUNSUPPORTED;
+  }
+  return RET_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ret_norm_gate(const void* y, const void* gate, void* o, int B, int H, int N, int dv, int norm,
+                  float eps, int token_major, long long ldg, long long ldo, int dtype,
+                  void* stream) {
+  long long* pitches[] = {&ldg, &ldo};
+  int s = check_norm_gate(B, H, N, dv, norm, eps, token_major, dtype, pitches, 2);
+  if (s) return s;
+  if (N == 0) return RET_OK;
+  if (!y || !o || !aligned16(y) || !aligned16(o) || !aligned16(gate)) return RET_EINVAL;
+  const int64_t rows = (int64_t)B * N, es = elem_bytes(dtype), w = (int64_t)H * dv * es;
+  // head-major arrays, and token-major ones of one head, have y's layout
+  const bool like_y = !token_major || H == 1;
+  const Extent in[] = {{y, 1, 0, rows, w, w}, {gate, 1, 0, rows, ldg * es, w}};
+  const Extent out[] = {{o, 1, 0, rows, ldo * es, w}};
+  if (clash(out, 1, in, 2, [&](int, int i) { return i == 1 || like_y; })) return RET_EINVAL;
+  ret::NormGateArgs a = {};
+  a.y = y, a.gate = gate, a.o = o, a.ldg = ldg, a.ldo = ldo;
+  a.B = B, a.H = H, a.N = N, a.dv = dv, a.norm = norm, a.token_major = token_major != 0;
+  a.dtype = dtype, a.eps = eps;
+  return cuda_status(ret::launch_norm_gate(a, static_cast<cudaStream_t>(stream)));
+}
+
+int ret_norm_gate_backward(const void* y, const void* gate, const void* d_o, void* grad_y,
+                           void* grad_gate, int B, int H, int N, int dv, int norm, float eps,
+                           int token_major, long long ldg, long long lddo, long long ldgg,
+                           int dtype, void* stream) {
+  long long* pitches[] = {&ldg, &lddo, &ldgg};
+  int s = check_norm_gate(B, H, N, dv, norm, eps, token_major, dtype, pitches, 3);
+  if (s) return s;
+  if (N == 0) return RET_OK;
+  if (!gate) grad_gate = nullptr;
+  if (!y || !d_o || !grad_y || (gate && !grad_gate)) return RET_EINVAL;
+  if (!aligned16(y) || !aligned16(gate) || !aligned16(d_o) || !aligned16(grad_y) ||
+      !aligned16(grad_gate))
+    return RET_EINVAL;
+  const int64_t rows = (int64_t)B * N, es = elem_bytes(dtype), w = (int64_t)H * dv * es;
+  const Extent in[] = {{y, 1, 0, rows, w, w},
+                       {gate, 1, 0, rows, ldg * es, w},
+                       {d_o, 1, 0, rows, lddo * es, w}};
+  const Extent out[] = {{grad_y, 1, 0, rows, w, w}, {grad_gate, 1, 0, rows, ldgg * es, w}};
+  if (clash(out, 2, in, 3, [](int o, int i) { return o == 0 ? i == 0 : i > 0; }))
+    return RET_EINVAL;
+  ret::NormGateArgs a = {};
+  a.y = y, a.gate = gate, a.d_o = d_o, a.grad_y = grad_y, a.grad_gate = grad_gate;
+  a.ldg = ldg, a.ldo = lddo, a.ldgg = ldgg;
+  a.B = B, a.H = H, a.N = N, a.dv = dv, a.norm = norm, a.token_major = token_major != 0;
+  a.dtype = dtype, a.eps = eps;
+  return cuda_status(ret::launch_norm_gate_backward(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+int check_add_norm(long long rows, int d, int post_norm, int norm, float alpha, float beta,
+                   float eps, int dtype, const float* w_post, const float* w) {
+  if (rows < 0 || d < 1 || !valid_dtype(dtype)) return RET_EINVAL;
+  if (!norm_kind(norm) || (post_norm != RET_NORM_NONE && !norm_kind(post_norm)))
+    return RET_EINVAL;
+  if (!(eps >= 0.0f) || isinf(eps) || !isfinite(alpha) || !isfinite(beta)) return RET_EINVAL;
+  if (!aligned16(w_post) || !aligned16(w)) return RET_EINVAL;
+  if (d > 16384 || rows > INT32_MAX || rows > ((int64_t)1 << 40) / d) return RET_EUNSUPPORTED;
+  return RET_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ret_add_norm(const void* x, const void* residual, const float* w_post, const float* w,
+                 void* res_out, void* y, long long rows, int d, int post_norm, int norm,
+                 float alpha, float beta, float eps, int dtype, void* stream) {
+  int s = check_add_norm(rows, d, post_norm, norm, alpha, beta, eps, dtype, w_post, w);
+  if (s) return s;
+  if (rows == 0) return RET_OK;
+  if (!x || !res_out || !y) return RET_EINVAL;
+  for (const void* p : {x, residual, (const void*)res_out, (const void*)y})
+    if (!aligned_elem(p, dtype)) return RET_EINVAL;
+  const int64_t bytes = rows * d * elem_bytes(dtype);
+  const Extent in[] = {flat(x, bytes), flat(residual, bytes), flat(w_post, 4 * (int64_t)d),
+                       flat(w, 4 * (int64_t)d)};
+  const Extent out[] = {flat(res_out, bytes), flat(y, bytes)};
+  if (clash(out, 2, in, 4, [](int, int i) { return i < 2; })) return RET_EINVAL;
+  ret::AddNormArgs a = {};
+  a.x = x, a.residual = residual, a.w_post = w_post, a.w = w, a.res_out = res_out, a.y = y;
+  a.rows = rows, a.d = d, a.post_norm = post_norm, a.norm = norm, a.dtype = dtype;
+  a.alpha = alpha, a.beta = beta, a.eps = eps;
+  return cuda_status(ret::launch_add_norm(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t ret_add_norm_backward_workspace(long long rows, int d) {
+  if (check_add_norm(rows, d, RET_NORM_NONE, RET_NORM_RMS, 1.0f, 1.0f, 0.0f, RET_F32, nullptr,
+                     nullptr) != RET_OK)
+    return 0;
+  return ret::add_norm_backward_workspace_bytes(rows, d);
+}
+
+int ret_add_norm_backward(const void* x, const void* res_out, const float* w_post, const float* w,
+                          const void* d_y, const void* d_res_out, void* grad_x,
+                          void* grad_residual, float* grad_w, float* grad_w_post, long long rows,
+                          int d, int post_norm, int norm, float alpha, float beta, float eps,
+                          int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  int s = check_add_norm(rows, d, post_norm, norm, alpha, beta, eps, dtype, w_post, w);
+  if (s) return s;
+  if (!aligned4(grad_w) || !aligned4(grad_w_post)) return RET_EINVAL;
+  const int64_t bytes = rows * d * elem_bytes(dtype), wbytes = 4 * (int64_t)d;
+  if (grad_w && overlap(flat(grad_w, wbytes), flat(grad_w_post, wbytes))) return RET_EINVAL;
+  if (rows == 0) {
+    s = pass_state(nullptr, grad_w, d, stream);
+    return s ? s : pass_state(nullptr, grad_w_post, d, stream);
+  }
+  const bool need_x = post_norm != RET_NORM_NONE || grad_w_post;
+  if (!need_x) x = nullptr;
+  if (!res_out || !d_y || (need_x && !x)) return RET_EINVAL;
+  for (const void* p : {x, res_out, d_y, d_res_out, (const void*)grad_x,
+                        (const void*)grad_residual})
+    if (!aligned_elem(p, dtype)) return RET_EINVAL;
+  const size_t need = grad_w || grad_w_post ? ret_add_norm_backward_workspace(rows, d) : 0;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return RET_EWORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return RET_EINVAL;
+  const Extent in[] = {flat(x, bytes),         flat(res_out, bytes),  flat(d_y, bytes),
+                       flat(d_res_out, bytes), flat(w_post, wbytes), flat(w, wbytes)};
+  const Extent out[] = {flat(grad_x, bytes), flat(grad_residual, bytes), flat(grad_w, wbytes),
+                        flat(grad_w_post, wbytes), flat(workspace, (int64_t)need)};
+  if (clash(out, 5, in, 6, [](int o, int i) { return o < 2 && i < 4; })) return RET_EINVAL;
+  ret::AddNormArgs a = {};
+  a.x = x, a.w_post = w_post, a.w = w, a.res_out = const_cast<void*>(res_out), a.d_y = d_y;
+  a.d_res_out = d_res_out, a.grad_x = grad_x, a.grad_residual = grad_residual;
+  a.grad_w = grad_w, a.grad_w_post = grad_w_post;
+  a.rows = rows, a.d = d, a.post_norm = post_norm, a.norm = norm, a.dtype = dtype;
+  a.alpha = alpha, a.beta = beta, a.eps = eps;
+  return cuda_status(ret::launch_add_norm_backward(a, static_cast<float*>(workspace),
+                                                   static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

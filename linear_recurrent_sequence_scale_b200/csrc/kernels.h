@@ -54,6 +54,51 @@ cudaError_t launch_state_combine(const float* locals, const int* spans, int r,
 cudaError_t launch_rotate(const void* x, void* y, const float* theta, long long pos0, int B,
                           int H, int N, int d, int dtype, cudaStream_t st);
 
+// Gated linear recurrence (scan.cu): the arguments of ret_scan, its backward
+// and its step, each call reading those it has.  An operand's element (b, t, d)
+// is at b * batch + t * token + d.
+struct Operand {
+  void* p;
+  long long batch, token;
+};
+struct ScanArgs {
+  Operand x, f, gate, y, d_y, grad_x, grad_f, grad_gate;
+  const float *state_in, *d_state_out;
+  float *state_out, *d_state_in, *chunk_states;
+  int B, N, D, form, dtype;
+  void* workspace;
+};
+size_t scan_workspace_bytes(int B, int N, int D, int dtype);
+cudaError_t launch_scan(const ScanArgs& a, cudaStream_t st);
+cudaError_t launch_scan_backward(const ScanArgs& a, cudaStream_t st);
+cudaError_t launch_scan_step(const ScanArgs& a, cudaStream_t st);
+
+// Per-head norm and output gate as a pass of its own (norm_gate.cu).
+struct NormGateArgs {
+  const void *y, *gate, *d_o;
+  void *o, *grad_y, *grad_gate;
+  long long ldg, ldo, ldgg;  // ldo: also d_o
+  int B, H, N, dv, norm, token_major, dtype;
+  float eps;
+};
+cudaError_t launch_norm_gate(const NormGateArgs& a, cudaStream_t st);
+cudaError_t launch_norm_gate_backward(const NormGateArgs& a, cudaStream_t st);
+
+// Residual sum with the norms around it (add_norm.cu).  res_out is an output
+// of the forward and an input of the backward.
+struct AddNormArgs {
+  const void *x, *residual, *d_y, *d_res_out;
+  const float *w_post, *w;
+  void *res_out, *y, *grad_x, *grad_residual;
+  float *grad_w, *grad_w_post;
+  long long rows;
+  int d, post_norm, norm, dtype;
+  float alpha, beta, eps;
+};
+size_t add_norm_backward_workspace_bytes(long long rows, int d);
+cudaError_t launch_add_norm(const AddNormArgs& a, cudaStream_t st);
+cudaError_t launch_add_norm_backward(const AddNormArgs& a, float* ws, cudaStream_t st);
+
 cudaError_t launch_simt_parallel(const void* q, const void* k, const void* v, const float* gammas,
                                  const void* gate, void* o, int B, int H, int N, int dk, int dv,
                                  int dtype, float eps, cudaStream_t st);
