@@ -75,8 +75,9 @@ int ret_device_error(void) {
   const int a = ret::tc_state_device_error();
   const int b = ret::tc_out_device_error();
   const int c = ret::selftest_device_error();
-  if (a < 0 || b < 0 || c < 0) return -1;
-  return a ? a : (b ? b : c);
+  const int d = ret::scan_device_error();
+  if (a < 0 || b < 0 || c < 0 || d < 0) return -1;
+  return a ? a : (b ? b : (c ? c : d));
 }
 
 int ret_selftest_bounded_wait(int limit_ms, void* stream) {
@@ -532,6 +533,9 @@ int check_scan(int B, int N, int D, int form, int dtype) {
   const int64_t channels = (int64_t)B * D;
   if (channels > INT32_MAX) return RET_EUNSUPPORTED;
   if (N > 0 && channels > ((int64_t)1 << 40) / N) return RET_EUNSUPPORTED;
+  // items of 64 tokens x 32 channels are counted in an int
+  const int64_t items = (int64_t)B * ((D + 31) / 32) * (((int64_t)N + 63) / 64);
+  if (items > ((int64_t)1 << 30)) return RET_EUNSUPPORTED;
   return RET_OK;
 }
 

@@ -69,6 +69,7 @@ struct ScanArgs {
   void* workspace;
 };
 size_t scan_workspace_bytes(int B, int N, int D, int dtype);
+int scan_device_error();
 cudaError_t launch_scan(const ScanArgs& a, cudaStream_t st);
 cudaError_t launch_scan_backward(const ScanArgs& a, cudaStream_t st);
 cudaError_t launch_scan_step(const ScanArgs& a, cudaStream_t st);
