@@ -9,11 +9,13 @@
 // replaced by a gate of the input and the d_k x d_v state by one value per
 // channel.
 //
-// The decay is kept as its complement and applied as h - c h: a decay close
-// to 1 rounded to float32 would be off by up to 2^-25 every token, the same
-// way each time where the gate is steady, while c carries full relative
-// precision.  fma(-c, h, h) is exactly 0 at c = 1, so a token with a zero
-// decay drops all that was before it.
+// The decay is kept as q = a - 1 and applied as h + q h: a decay close to 1
+// rounded to float32 would be off by up to 2^-25 every token, the same way
+// each time where the gate is steady, while q carries full relative
+// precision.  fma(q, h, h) is exactly 0 at q = -1, so a token with a zero
+// decay drops all that was before it.  The state itself is carried as z = h
+// (LOG) or z = -h (LOGIT), which makes a step two fused operations without a
+// negation: z + q z + x, and z + q z + q x.
 #include "common.cuh"
 #include "kernels.h"
 #include "rowvec.cuh"
@@ -22,31 +24,104 @@
 namespace ret {
 namespace scan {
 
-// 1 - a.  LOGIT: sigmoid(-f) from e^-|f|, which cannot overflow.  LOG:
-// 1 - e^f, by the Taylor series of e^f - 1 where the difference would cancel
-// (|f| < 1/4: seven terms leave 5e-8 of the value).
-template <int FORM>
-__device__ __forceinline__ float complement(float f) {
+// The n = 1 or 2 channels that a lane computes together; two go through the
+// paired float32 instructions, which hold the kernels' issue rate under what
+// HBM asks for (one element takes about 12 instruction slots forwards; at
+// 6.5 TB/s there are 31).
+template <int n> struct Vec {
+  float v[n];
+};
+template <int n> __device__ __forceinline__ Vec<n> all(float x) {
+  Vec<n> r;
+#pragma unroll
+  for (int i = 0; i < n; ++i) r.v[i] = x;
+  return r;
+}
+__device__ __forceinline__ Vec<1> fma(Vec<1> a, Vec<1> b, Vec<1> c) {
+  return {{fmaf(a.v[0], b.v[0], c.v[0])}};
+}
+__device__ __forceinline__ Vec<2> fma(Vec<2> a, Vec<2> b, Vec<2> c) {
+  Vec<2> r;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.v[0]), "=f"(r.v[1])
+      : "f"(a.v[0]), "f"(a.v[1]), "f"(b.v[0]), "f"(b.v[1]), "f"(c.v[0]), "f"(c.v[1]));
+  return r;
+}
+__device__ __forceinline__ Vec<1> add(Vec<1> a, Vec<1> b) { return {{a.v[0] + b.v[0]}}; }
+__device__ __forceinline__ Vec<2> add(Vec<2> a, Vec<2> b) {
+  Vec<2> r;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.v[0]), "=f"(r.v[1])
+      : "f"(a.v[0]), "f"(a.v[1]), "f"(b.v[0]), "f"(b.v[1]));
+  return r;
+}
+__device__ __forceinline__ Vec<1> mul(Vec<1> a, Vec<1> b) { return {{a.v[0] * b.v[0]}}; }
+__device__ __forceinline__ Vec<2> mul(Vec<2> a, Vec<2> b) {
+  Vec<2> r;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.v[0]), "=f"(r.v[1])
+      : "f"(a.v[0]), "f"(a.v[1]), "f"(b.v[0]), "f"(b.v[1]));
+  return r;
+}
+
+// 2^x and 1/x by the hardware's approximations (2 and 1 units in the last
+// place); 1/x of an infinity is 0.
+template <int n> __device__ __forceinline__ Vec<n> exp2v(Vec<n> x) {
+#pragma unroll
+  for (int i = 0; i < n; ++i) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x.v[i]) : "f"(x.v[i]));
+  return x;
+}
+template <int n> __device__ __forceinline__ Vec<n> rcpv(Vec<n> x) {
+#pragma unroll
+  for (int i = 0; i < n; ++i) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(x.v[i]) : "f"(x.v[i]));
+  return x;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// q = a - 1.  LOGIT: -1 / (1 + e^f), of full relative precision for every f
+// (an overflow of e^f gives 0).  LOG: e^f - 1, by its Taylor series where the
+// difference would cancel (|f| < 1/4: six terms leave 5e-8 of the value).
+template <int FORM, int n> __device__ __forceinline__ Vec<n> less_one(Vec<n> f) {
+  const Vec<n> e = exp2v(mul(f, all<n>(kLog2e)));
   if constexpr (FORM == RET_SCAN_LOGIT) {
-    const float e = __expf(-fabsf(f));
-    const float r = __fdividef(1.0f, 1.0f + e);
-    return f >= 0.0f ? e * r : r;
+    return rcpv(fma(e, all<n>(-1.0f), all<n>(-1.0f)));
   } else {
-    float s = fmaf(f, 1.0f / 720.0f, 1.0f / 120.0f);
-    s = fmaf(f, s, 1.0f / 24.0f);
-    s = fmaf(f, s, 1.0f / 6.0f);
-    s = fmaf(f, s, 0.5f);
-    s = fmaf(f, s, 1.0f);
-    return fabsf(f) < 0.25f ? -f * s : 1.0f - __expf(f);
+    Vec<n> s = fma(f, all<n>(1.0f / 720.0f), all<n>(1.0f / 120.0f));
+    s = fma(f, s, all<n>(1.0f / 24.0f));
+    s = fma(f, s, all<n>(1.0f / 6.0f));
+    s = fma(f, s, all<n>(0.5f));
+    s = fma(f, s, all<n>(1.0f));
+    s = mul(f, s);
+    Vec<n> q = add(e, all<n>(-1.0f));
+#pragma unroll
+    for (int i = 0; i < n; ++i) q.v[i] = fabsf(f.v[i]) < 0.25f ? s.v[i] : q.v[i];
+    return q;
   }
 }
 
-// h_t from h_{t-1}, the complement c and the input x.
-template <int FORM>
-__device__ __forceinline__ float advance(float h, float c, float x) {
-  const float kept = fmaf(-c, h, h);
-  return FORM == RET_SCAN_LOGIT ? fmaf(c, x, kept) : kept + x;
+// z from the state h and back.
+template <int FORM> __device__ __forceinline__ float turn(float h) {
+  return FORM == RET_SCAN_LOGIT ? -h : h;
 }
+
+// z after a token.
+template <int FORM, int n>
+__device__ __forceinline__ Vec<n> advance(Vec<n> z, Vec<n> q, Vec<n> x) {
+  const Vec<n> kept = fma(q, z, z);
+  return FORM == RET_SCAN_LOGIT ? fma(q, x, kept) : add(kept, x);
+}
+
+// swish(g) and, times dy, what d swish(g) takes and what passes on to h.
+template <int n> __device__ __forceinline__ Vec<n> sigmoid(Vec<n> g) {
+  return rcpv(add(exp2v(mul(g, all<n>(-kLog2e))), all<n>(1.0f)));
+}
+template <int n> __device__ __forceinline__ Vec<n> swish(Vec<n> g) { return mul(g, sigmoid(g)); }
 
 constexpr int kThreads = 128;  // of the single-token kernel
 
@@ -58,18 +133,17 @@ __device__ __forceinline__ T* at(const Operand& o, long long b, long long t, lon
 
 // ---- sequence form ------------------------------------------------------------
 //
-// The recurrence composes: a span of tokens turns the state s before it into
-// H + s - C s, where H is its end state from zero and 1 - C the product of
-// its decays (kept as C for the reason above: C <- C + c (1 - C) per token).
+// The recurrence composes: a span of tokens turns the z before it into
+// Z + z + Q z, where Z is its end from zero and 1 + Q the product of its
+// decays (kept as Q for the reason above: Q <- Q + q Q + q per token).
 // The sequence is cut into items of kTok tokens x one 128-byte piece of
 // channels.  A block keeps a ring of items in shared memory (loads of the
 // next ones run while one is computed), and per item
 //   1. each of 8 warps scans its own kTok/8 tokens from zero, channels across
-//      lanes (4 bytes of them each), and leaves (C, H) in shared memory;
-//   2. warp 0 folds the eight, publishes the item's (C, H), looks back over
+//      lanes (4 bytes of them each), and leaves (Q, Z) in shared memory;
+//   2. warp 0 folds the eight, publishes the item's (Q, Z), looks back over
 //      the previous items of the same channels until it meets one whose end
-//      state is published, folds forward from there, and publishes its own
-//      end state;
+//      is published, folds forward from there, and publishes its own end;
 //   3. every warp runs its tokens again from the state that enters them and
 //      writes y.
 // So every element crosses HBM once, and neither few channels nor long
@@ -81,8 +155,8 @@ __device__ __forceinline__ T* at(const Operand& o, long long b, long long t, lon
 // GPU runs.  The wait is bounded in time all the same.  A published word is
 // its own flag (every word of the workspace starts as kEmpty, which no
 // result of arithmetic is), so no fence or lock is needed, and folding from
-// any published end state gives the same bits: the end state of an item is
-// itself the fold of its (C, H) over the one before.
+// any published end gives the same bits: the end of an item is itself the fold
+// of its (Q, Z) over the one before.
 constexpr int kWarps = 8;
 constexpr int kBlock = 32 * kWarps;
 constexpr int kPiece = 128;                // bytes of one row of an item
@@ -92,8 +166,8 @@ constexpr int kSiteForward = 801, kSiteBackward = 802;
 
 struct Plan {
   int* ticket;     // starts at -1 (all bits set, like the rest of the workspace)
-  float* end;      // [tile][B][blocks][channels]: end states
-  float2* span;    // same: (C, H)
+  float* end;      // [tile][B][blocks][channels]: what leaves an item
+  float* span;     // same, two words per channel: a lane's Q's, then its Z's
   int blocks;      // pieces of channels per batch row
   int tiles;       // items per piece
   int items;
@@ -102,49 +176,79 @@ struct Plan {
 __device__ __forceinline__ float word(float x) {
   return __float_as_uint(x) == kEmpty ? __uint_as_float(0x7fffffffu) : x;
 }
-__device__ __forceinline__ bool written(float x) { return __float_as_uint(x) != kEmpty; }
-__device__ __forceinline__ float ld_word(const float* p) {
-  float v;
-  asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
-  return v;
+template <int n> __device__ __forceinline__ bool written(const Vec<n>& x) {
+  bool r = true;
+#pragma unroll
+  for (int i = 0; i < n; ++i) r = r && __float_as_uint(x.v[i]) != kEmpty;
+  return r;
 }
-__device__ __forceinline__ float2 ld_words(const float2* p) {
-  float2 v;
+// Words are read and written one by one as far as their meaning goes; the
+// vector forms only save instructions.
+__device__ __forceinline__ void ld_words(const float* p, Vec<1>& a) {
+  asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(a.v[0]) : "l"(p) : "memory");
+}
+__device__ __forceinline__ void ld_words(const float* p, Vec<2>& a) {
   asm volatile("ld.relaxed.gpu.global.v2.f32 {%0, %1}, [%2];"
-               : "=f"(v.x), "=f"(v.y)
+               : "=f"(a.v[0]), "=f"(a.v[1])
                : "l"(p)
                : "memory");
-  return v;
 }
-__device__ __forceinline__ void st_word(float* p, float v) {
-  asm volatile("st.relaxed.gpu.global.f32 [%0], %1;" ::"l"(p), "f"(word(v)) : "memory");
+__device__ __forceinline__ void ld_words(const float* p, Vec<1>& a, Vec<1>& b) {
+  asm volatile("ld.relaxed.gpu.global.v2.f32 {%0, %1}, [%2];"
+               : "=f"(a.v[0]), "=f"(b.v[0])
+               : "l"(p)
+               : "memory");
 }
-__device__ __forceinline__ void st_words(float2* p, float x, float y) {
-  asm volatile("st.relaxed.gpu.global.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(word(x)),
-               "f"(word(y))
+__device__ __forceinline__ void ld_words(const float* p, Vec<2>& a, Vec<2>& b) {
+  asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(a.v[0]), "=f"(a.v[1]), "=f"(b.v[0]), "=f"(b.v[1])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void st_words(float* p, Vec<1> a) {
+  asm volatile("st.relaxed.gpu.global.f32 [%0], %1;" ::"l"(p), "f"(word(a.v[0])) : "memory");
+}
+__device__ __forceinline__ void st_words(float* p, Vec<2> a) {
+  asm volatile("st.relaxed.gpu.global.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(word(a.v[0])),
+               "f"(word(a.v[1]))
+               : "memory");
+}
+__device__ __forceinline__ void st_words(float* p, Vec<1> a, Vec<1> b) {
+  asm volatile("st.relaxed.gpu.global.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(word(a.v[0])),
+               "f"(word(b.v[0]))
+               : "memory");
+}
+__device__ __forceinline__ void st_words(float* p, Vec<2> a, Vec<2> b) {
+  asm volatile("st.relaxed.gpu.global.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p),
+               "f"(word(a.v[0])), "f"(word(a.v[1])), "f"(word(b.v[0])), "f"(word(b.v[1]))
                : "memory");
 }
 
-// The state after a span (C, H) entered with s.
-__device__ __forceinline__ float fold(float s, float C, float H) { return fmaf(-C, s, s) + H; }
+// z after a span (Q, Z) entered with z, and the Q of a span and the one after.
+template <int n> __device__ __forceinline__ Vec<n> fold(Vec<n> z, Vec<n> Q, Vec<n> Z) {
+  return add(fma(Q, z, z), Z);
+}
+template <int n> __device__ __forceinline__ Vec<n> chain(Vec<n> Q, Vec<n> q) {
+  return add(fma(q, Q, Q), q);
+}
 
-// The state that enters item `tile` (> 0) of a channel: `at` points at the
-// channel's words of that item, `pitch` words from one tile to the next.
-__device__ __forceinline__ float look_back(const Plan& p, size_t at, size_t pitch, int tile,
-                                           int site) {
-  float s = 0.0f;
+// What enters item `tile` (> 0) of a lane's channels: `at` points at their
+// words of that item, `pitch` words from one tile to the next.
+template <int n>
+__device__ __forceinline__ Vec<n> look_back(const Plan& p, size_t at, size_t pitch, int tile,
+                                            int site) {
+  Vec<n> z = all<n>(0.0f);
   bool found = false;
   uint64_t t0 = 0;
   int tries = 0;
   while (true) {
-    float e[kWindow];
-    float2 g[kWindow];
+    Vec<n> e[kWindow], Q[kWindow], Z[kWindow];
 #pragma unroll
     for (int i = 0; i < kWindow; ++i) {
-      e[i] = __uint_as_float(kEmpty);
+      e[i] = all<n>(__uint_as_float(kEmpty));
       if (tile - 1 - i >= 0) {
-        e[i] = ld_word(p.end + at - (i + 1) * pitch);
-        if (i + 1 < kWindow) g[i] = ld_words(p.span + at - (i + 1) * pitch);
+        ld_words(p.end + at - (i + 1) * pitch, e[i]);
+        if (i + 1 < kWindow) ld_words(p.span + 2 * (at - (i + 1) * pitch), Q[i], Z[i]);
       }
     }
     // the nearest published end state, if every span after it is published
@@ -153,16 +257,15 @@ __device__ __forceinline__ float look_back(const Plan& p, size_t at, size_t pitc
 #pragma unroll
       for (int i = 0; i < kWindow; ++i) {
         if (!found && whole && written(e[i])) {
-          s = e[i];
+          z = e[i];
           found = true;
 #pragma unroll
-          for (int k = i - 1; k >= 0; --k) s = fold(s, g[k].x, g[k].y);
+          for (int k = i - 1; k >= 0; --k) z = fold(z, Q[k], Z[k]);
         }
-        if (i + 1 < kWindow && tile - 1 - i >= 0)
-          whole = whole && written(g[i].x) && written(g[i].y);
+        if (i + 1 < kWindow && tile - 1 - i >= 0) whole = whole && written(Q[i]) && written(Z[i]);
       }
     }
-    if (__all_sync(0xffffffffu, found)) return s;
+    if (__all_sync(0xffffffffu, found)) return z;
     if (++tries % 64 == 0) {
       const uint64_t now = sm100::globaltimer();
       if (t0 == 0) t0 = now;
@@ -170,7 +273,7 @@ __device__ __forceinline__ float look_back(const Plan& p, size_t at, size_t pitc
       if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&g_device_error) != 0 ||
                                       now - t0 > sm100::kWaitLimitNs)) {
         sm100::record_error(site);
-        return __uint_as_float(0x7fffffffu);
+        return all<n>(__uint_as_float(0x7fffffffu));
       }
     }
   }
@@ -224,23 +327,50 @@ __device__ __forceinline__ void copy_item(char* dst, const char* src, long long 
 }
 
 // The channels of one lane: 4 bytes of a row.
-template <typename T> struct Lane {
-  static constexpr int n = 4 / sizeof(T);
-  float v[n];
-  __device__ __forceinline__ void get(const char* row) {
-    load_pack<T, n>(reinterpret_cast<const T*>(row) + (threadIdx.x % 32) * n, v);
-  }
-  // `left`: channels of the piece that exist from this lane's first one on
-  template <bool PAIR> __device__ __forceinline__ void put(T* p, int left) const {
-    if (PAIR || n == 1) {
-      if (left > 0) store_pack<T, n>(p, v);
-    } else {
+template <typename T> constexpr int kLane = 4 / sizeof(T);
+template <typename T> __device__ __forceinline__ Vec<kLane<T>> get(const char* row) {
+  Vec<kLane<T>> r;
+  load_pack<T, kLane<T>>(reinterpret_cast<const T*>(row) + (threadIdx.x % 32) * kLane<T>, r.v);
+  return r;
+}
+// `left`: channels of the piece that exist from this lane's first one on.
+template <typename T, bool PAIR, int n>
+__device__ __forceinline__ void put(T* p, const Vec<n>& x, int left) {
+  if (PAIR || n == 1) {
+    if (left > 0) store_pack<T, n>(p, x.v);
+  } else {
 #pragma unroll
-      for (int i = 0; i < n; ++i)
-        if (i < left) Elem<T>::st(p + i, v[i]);
-    }
+    for (int i = 0; i < n; ++i)
+      if (i < left) Elem<T>::st(p + i, x.v[i]);
   }
-};
+}
+template <int n> __device__ __forceinline__ Vec<n> get_state(const float* p, int left) {
+  Vec<n> r;
+#pragma unroll
+  for (int i = 0; i < n; ++i) r.v[i] = p && i < left ? p[i] : 0.0f;
+  return r;
+}
+template <int n> __device__ __forceinline__ void put_state(float* p, const Vec<n>& x, int left) {
+#pragma unroll
+  for (int i = 0; i < n; ++i)
+    if (i < left) p[i] = x.v[i];
+}
+template <int FORM, int n> __device__ __forceinline__ Vec<n> turn(Vec<n> h) {
+#pragma unroll
+  for (int i = 0; i < n; ++i) h.v[i] = turn<FORM>(h.v[i]);
+  return h;
+}
+// Rows past the end of a sequence hold zeros, which is a decay of 1 and no
+// input for LOG; LOGIT needs its gate at +inf for that.
+template <int FORM, typename T>
+__device__ __forceinline__ void open_gates(char* f, int rows, int tok) {
+  if (FORM == RET_SCAN_LOGIT && rows < tok) {
+    const uint32_t inf = sizeof(T) == 2 ? 0x7f807f80u : 0x7f800000u;
+    for (int i = rows * (kPiece / 4) + threadIdx.x; i < tok * (kPiece / 4); i += kBlock)
+      reinterpret_cast<uint32_t*>(f)[i] = inf;
+    __syncthreads();
+  }
+}
 
 constexpr int kTokForward = 128, kTokBackward = RET_SCAN_CHUNK;
 static_assert(kTokForward % RET_SCAN_CHUNK == 0, "chunk states are kept at warp boundaries");
@@ -262,12 +392,12 @@ template <int STAGES> struct Items {
 
 template <typename T, int FORM, bool GATE, int W>
 __global__ void __launch_bounds__(kBlock, 2) scan_items(const ScanArgs a, const Plan p) {
-  using L = Lane<T>;
   using R = Ring<GATE ? 3 : 2, kTokForward>;
-  constexpr int n = L::n, kTok = kTokForward, S = kTok / kWarps, C = 32 * n;
+  constexpr int n = kLane<T>, kTok = kTokForward, S = kTok / kWarps, C = 32 * n;
+  using V = Vec<n>;
   extern __shared__ __align__(128) char ring[];
   __shared__ Items<R::kStages> items;
-  __shared__ float agg_c[kWarps][C], agg_h[kWarps][C], enter[C];
+  __shared__ V agg_q[kWarps][32], agg_z[kWarps][32], enter[32];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const size_t pitch = (size_t)a.B * p.blocks * C;
   const int pieces = a.B * p.blocks;
@@ -310,98 +440,61 @@ __global__ void __launch_bounds__(kBlock, 2) scan_items(const ScanArgs a, const 
                       : (int)(blockIdx.x + (k + R::kStages) * gridDim.x);
     cp_wait<R::kStages - 1>();
     __syncthreads();
+    open_gates<FORM, T>(ring + slot * R::kStage, rows, kTok);
     const char* f = ring + slot * R::kStage + warp * S * kPiece;
     const char* x = f + R::kOperand;
 
-    // 1. this warp's tokens from zero; tokens past the end change nothing
-    float c[S][n], C_w[n], H_w[n];
-#pragma unroll
-    for (int i = 0; i < n; ++i) C_w[i] = H_w[i] = 0.0f;
+    // 1. this warp's tokens from zero
+    V q[S], Q = all<n>(0.0f), Z = Q;
 #pragma unroll
     for (int j = 0; j < S; ++j) {
-      L fv, xv;
-      fv.get(f + j * kPiece);
-      xv.get(x + j * kPiece);
-#pragma unroll
-      for (int i = 0; i < n; ++i) {
-        c[j][i] = warp * S + j < rows ? complement<FORM>(fv.v[i]) : 0.0f;
-        H_w[i] = advance<FORM>(H_w[i], c[j][i], xv.v[i]);
-        C_w[i] = fmaf(c[j][i], 1.0f - C_w[i], C_w[i]);
-      }
+      q[j] = less_one<FORM>(get<T>(f + j * kPiece));
+      Z = advance<FORM>(Z, q[j], get<T>(x + j * kPiece));
+      Q = chain(Q, q[j]);
     }
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-      agg_c[warp][lane * n + i] = C_w[i];
-      agg_h[warp][lane * n + i] = H_w[i];
-    }
+    agg_q[warp][lane] = Q;
+    agg_z[warp][lane] = Z;
     __syncthreads();
 
-    // 2. the state that enters the item
+    // 2. what enters the item (warp 0), and the span of the warps before
+    Q = all<n>(0.0f), Z = Q;
+    for (int w = 0; w < (warp == 0 ? kWarps : warp); ++w) {
+      Z = fold(Z, agg_q[w][lane], agg_z[w][lane]);
+      Q = chain(Q, agg_q[w][lane]);
+    }
+    V z;
     if (warp == 0) {
-#pragma unroll
-      for (int i = 0; i < n; ++i) {
-        float C_t = 0.0f, H_t = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float cw = agg_c[w][lane * n + i];
-          H_t = fold(H_t, cw, agg_h[w][lane * n + i]);
-          C_t = fmaf(cw, 1.0f - C_t, C_t);
-        }
-        C_w[i] = C_t, H_w[i] = H_t;
-        if (tile > 0 && tile + 1 < p.tiles) st_words(p.span + words + i, C_t, H_t);
+      if (tile > 0) {
+        if (tile + 1 < p.tiles) st_words(p.span + 2 * words, Q, Z);
+        z = look_back<n>(p, words, pitch, tile, kSiteForward);
+      } else {
+        z = turn<FORM>(get_state<n>(a.state_in ? a.state_in + (size_t)b * a.D + d : nullptr, left));
       }
-#pragma unroll
-      for (int i = 0; i < n; ++i) {
-        float s;
-        if (tile > 0)
-          s = look_back(p, words + i, pitch, tile, kSiteForward);
-        else
-          s = a.state_in && i < left ? a.state_in[(size_t)b * a.D + d + i] : 0.0f;
-        if (tile + 1 < p.tiles) st_word(p.end + words + i, fold(s, C_w[i], H_w[i]));
-        enter[lane * n + i] = s;
-      }
+      if (tile + 1 < p.tiles) st_words(p.end + words, fold(z, Q, Z));
+      enter[lane] = z;
     }
     __syncthreads();
 
-    // 3. the same tokens from the state that enters them
-    float h[n];
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-      h[i] = enter[lane * n + i];
-      for (int w = 0; w < warp; ++w)
-        h[i] = fold(h[i], agg_c[w][lane * n + i], agg_h[w][lane * n + i]);
-    }
+    // 3. the same tokens from the z that enters them
+    if (warp > 0) z = fold(enter[lane], Q, Z);
     const int t0 = tile * kTok + warp * S, mine = min(S, a.N - t0);
-    if (a.chunk_states && t0 % RET_SCAN_CHUNK == 0 && mine > 0) {
-      float* keep = a.chunk_states +
-                    ((size_t)b * cdiv(a.N, RET_SCAN_CHUNK) + t0 / RET_SCAN_CHUNK) * a.D + d;
-#pragma unroll
-      for (int i = 0; i < n; ++i)
-        if (i < left) keep[i] = h[i];
-    }
+    if (a.chunk_states && t0 % RET_SCAN_CHUNK == 0 && mine > 0)
+      put_state(a.chunk_states +
+                    ((size_t)b * cdiv(a.N, RET_SCAN_CHUNK) + t0 / RET_SCAN_CHUNK) * a.D + d,
+                turn<FORM>(z), left);
     T* y = at<T>(a.y, b, t0, d);
 #pragma unroll
     for (int j = 0; j < S; ++j) {
       if (j < mine) {
-        L xv, out;
-        xv.get(x + j * kPiece);
-#pragma unroll
-        for (int i = 0; i < n; ++i) out.v[i] = h[i] = advance<FORM>(h[i], c[j][i], xv.v[i]);
-        if constexpr (GATE) {
-          L g;
-          g.get(f + 2 * R::kOperand + j * kPiece);
-#pragma unroll
-          for (int i = 0; i < n; ++i) out.v[i] *= g.v[i] * sigmoidf(g.v[i]);
-        }
-        out.template put<(W >= 4)>(y, left);
+        z = advance<FORM>(z, q[j], get<T>(x + j * kPiece));
+        V out = turn<FORM>(z);
+        if constexpr (GATE) out = mul(out, swish(get<T>(f + 2 * R::kOperand + j * kPiece)));
+        put<T, (W >= 4)>(y, out, left);
         y += a.y.token;
       }
     }
-    if (a.state_out && mine > 0 && t0 + mine == a.N) {
-#pragma unroll
-      for (int i = 0; i < n; ++i)
-        if (i < left) a.state_out[(size_t)b * a.D + d + i] = h[i];
-    }
+    if (a.state_out && mine > 0 && t0 + mine == a.N)
+      put_state(a.state_out + (size_t)b * a.D + d, turn<FORM>(z), left);
     if (threadIdx.x == 0) items.take[slot] = next;
     __syncthreads();
     load(slot);
@@ -418,20 +511,20 @@ __global__ void __launch_bounds__(kBlock, 2) scan_items(const ScanArgs a, const 
 //     dg_t = dy_t h_t swish'(g_t),   d state_in = a_0 G_0.
 // What flows to the token before, E_t = a_t G_t, obeys the same kind of
 // recurrence in reversed time: a span turns the flow e behind it into
-// E + e - C e with the same C.  So the items are taken from the end of the
+// E + e + Q e with the same Q.  So the items are taken from the end of the
 // sequence, of one chunk each: the state that enters the chunk comes from the
 // forward call, h is recomputed in float32 inside it, and the flow is looked
 // for in the items after it as the forward does in those before.
 template <typename T, int FORM, bool GATE, int W>
 __global__ void __launch_bounds__(kBlock, 2) scan_items_backward(const ScanArgs a, const Plan p) {
-  using L = Lane<T>;
   using R = Ring<GATE ? 4 : 3, kTokBackward>;
-  constexpr int n = L::n, kTok = kTokBackward, S = kTok / kWarps, C = 32 * n;
+  constexpr int n = kLane<T>, kTok = kTokBackward, S = kTok / kWarps, C = 32 * n;
+  using V = Vec<n>;
   constexpr int kX = R::kOperand, kDy = 2 * R::kOperand, kGate = 3 * R::kOperand;
   constexpr int kState = (GATE ? 4 : 3) * R::kOperand;
   extern __shared__ __align__(128) char ring[];
   __shared__ Items<R::kStages> items;
-  __shared__ float agg_c[kWarps][C], agg_h[kWarps][C], agg_e[kWarps][C], leave[C];
+  __shared__ V agg_q[kWarps][32], agg_z[kWarps][32], agg_e[kWarps][32], leave[32];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const size_t pitch = (size_t)a.B * p.blocks * C;
   const int pieces = a.B * p.blocks;
@@ -483,127 +576,92 @@ __global__ void __launch_bounds__(kBlock, 2) scan_items_backward(const ScanArgs 
     cp_wait<R::kStages - 1>();
     __syncthreads();
     const char* stage = ring + slot * R::kStage;
+    open_gates<FORM, T>(ring + slot * R::kStage, rows, kTok);
     const char* f = stage + warp * S * kPiece;
 
     // 1. this warp's tokens: forwards from a zero state, backwards from a zero flow
-    float c[S][n], dh[S][n], slope[GATE ? S : 1][n], C_w[n], H_w[n], E_w[n];
-#pragma unroll
-    for (int i = 0; i < n; ++i) C_w[i] = H_w[i] = E_w[i] = 0.0f;
+    V q[S], dh[S], slope[GATE ? S : 1], Q = all<n>(0.0f), Z = Q, E = Q;
 #pragma unroll
     for (int j = 0; j < S; ++j) {
-      L fv, xv, dv;
-      fv.get(f + j * kPiece);
-      xv.get(f + kX + j * kPiece);
-      dv.get(f + kDy + j * kPiece);
-#pragma unroll
-      for (int i = 0; i < n; ++i) {
-        c[j][i] = warp * S + j < rows ? complement<FORM>(fv.v[i]) : 0.0f;
-        H_w[i] = advance<FORM>(H_w[i], c[j][i], xv.v[i]);
-        C_w[i] = fmaf(c[j][i], 1.0f - C_w[i], C_w[i]);
-        dh[j][i] = dv.v[i];
-      }
+      q[j] = less_one<FORM>(get<T>(f + j * kPiece));
+      Z = advance<FORM>(Z, q[j], get<T>(f + kX + j * kPiece));
+      Q = chain(Q, q[j]);
+      dh[j] = get<T>(f + kDy + j * kPiece);
       if constexpr (GATE) {
-        L g;
-        g.get(f + kGate + j * kPiece);
-#pragma unroll
-        for (int i = 0; i < n; ++i) {
-          float sw, sl;
-          swish_grad(g.v[i], &sw, &sl);
-          slope[j][i] = dh[j][i] * sl;
-          dh[j][i] *= sw;
-        }
+        const V g = get<T>(f + kGate + j * kPiece), sig = sigmoid(g), sw = mul(g, sig);
+        // swish'(g) = sig + sw (1 - sig), with the sign of z
+        const V rest = fma(sig, all<n>(-1.0f), all<n>(1.0f));
+        slope[j] = scan::turn<FORM>(mul(dh[j], fma(sw, rest, sig)));
+        dh[j] = mul(dh[j], sw);
       }
-    }
-#pragma unroll
-    for (int j = S - 1; j >= 0; --j)
-#pragma unroll
-      for (int i = 0; i < n; ++i) {
-        const float G = dh[j][i] + E_w[i];
-        E_w[i] = fmaf(-c[j][i], G, G);
-      }
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-      agg_c[warp][lane * n + i] = C_w[i];
-      agg_h[warp][lane * n + i] = H_w[i];
-      agg_e[warp][lane * n + i] = E_w[i];
-    }
-    __syncthreads();
-
-    // 2. the flow that reaches the item from behind
-    if (warp == 0) {
-#pragma unroll
-      for (int i = 0; i < n; ++i) {
-        float C_t = 0.0f, E_t = 0.0f;
-#pragma unroll
-        for (int w = kWarps - 1; w >= 0; --w) {
-          const float cw = agg_c[w][lane * n + i];
-          E_t = fold(E_t, cw, agg_e[w][lane * n + i]);
-          C_t = fmaf(cw, 1.0f - C_t, C_t);
-        }
-        C_w[i] = C_t, E_w[i] = E_t;
-        if (turn > 0 && turn + 1 < p.tiles) st_words(p.span + words + i, C_t, E_t);
-      }
-#pragma unroll
-      for (int i = 0; i < n; ++i) {
-        float s;
-        if (turn > 0)
-          s = look_back(p, words + i, pitch, turn, kSiteBackward);
-        else
-          s = a.d_state_out && i < left ? a.d_state_out[(size_t)b * a.D + d + i] : 0.0f;
-        if (turn + 1 < p.tiles) st_word(p.end + words + i, fold(s, C_w[i], E_w[i]));
-        leave[lane * n + i] = s;
-      }
-    }
-    __syncthreads();
-
-    // 3. h forwards from the state that enters, then the gradients backwards
-    const int t0 = tile * kTok + warp * S, mine = min(S, a.N - t0);
-    float h[n], before[S][n], flow[n];
-    const float* state = reinterpret_cast<const float*>(stage + kState);
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-      h[i] = state[lane * n + i];
-      for (int w = 0; w < warp; ++w)
-        h[i] = fold(h[i], agg_c[w][lane * n + i], agg_h[w][lane * n + i]);
-      flow[i] = leave[lane * n + i];
-      for (int w = kWarps - 1; w > warp; --w)
-        flow[i] = fold(flow[i], agg_c[w][lane * n + i], agg_e[w][lane * n + i]);
-    }
-#pragma unroll
-    for (int j = 0; j < S; ++j) {
-      L xv, dg;
-      xv.get(f + kX + j * kPiece);
-#pragma unroll
-      for (int i = 0; i < n; ++i) {
-        before[j][i] = h[i];
-        h[i] = advance<FORM>(h[i], c[j][i], xv.v[i]);
-        if constexpr (GATE) dg.v[i] = h[i] * slope[j][i];
-      }
-      if constexpr (GATE)
-        if (j < mine) dg.template put<(W >= 4)>(at<T>(a.grad_gate, b, t0 + j, d), left);
     }
 #pragma unroll
     for (int j = S - 1; j >= 0; --j) {
-      L xv, dx, df;
-      xv.get(f + kX + j * kPiece);
+      const V G = add(dh[j], E);
+      E = fma(q[j], G, G);
+    }
+    agg_q[warp][lane] = Q;
+    agg_z[warp][lane] = Z;
+    agg_e[warp][lane] = E;
+    __syncthreads();
+
+    // 2. the flow that reaches the item from behind (warp 0), and the span of
+    // the warps behind
+    Q = all<n>(0.0f), E = Q;
+    for (int w = kWarps - 1; w >= (warp == 0 ? 0 : warp + 1); --w) {
+      E = fold(E, agg_q[w][lane], agg_e[w][lane]);
+      Q = chain(Q, agg_q[w][lane]);
+    }
+    if (warp == 0) {
+      V e;
+      if (turn > 0) {
+        if (turn + 1 < p.tiles) st_words(p.span + 2 * words, Q, E);
+        e = look_back<n>(p, words, pitch, turn, kSiteBackward);
+      } else {
+        e = get_state<n>(a.d_state_out ? a.d_state_out + (size_t)b * a.D + d : nullptr, left);
+      }
+      if (turn + 1 < p.tiles) st_words(p.end + words, fold(e, Q, E));
+      leave[lane] = e;
+    }
+    // meanwhile z forwards from the state that enters the chunk
+    const int t0 = tile * kTok + warp * S, mine = min(S, a.N - t0);
+    V z, before[S];
 #pragma unroll
-      for (int i = 0; i < n; ++i) {
-        const float G = dh[j][i] + flow[i];
-        flow[i] = fmaf(-c[j][i], G, G);
-        dx.v[i] = FORM == RET_SCAN_LOGIT ? c[j][i] * G : G;
-        df.v[i] = FORM == RET_SCAN_LOGIT ? (before[j][i] - xv.v[i]) * c[j][i] * flow[i]
-                                         : before[j][i] * flow[i];
+    for (int i = 0; i < n; ++i)
+      z.v[i] = scan::turn<FORM>(reinterpret_cast<const float*>(stage + kState)[lane * n + i]);
+    for (int w = 0; w < warp; ++w) z = fold(z, agg_q[w][lane], agg_z[w][lane]);
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+      before[j] = z;
+      z = advance<FORM>(z, q[j], get<T>(f + kX + j * kPiece));
+      if constexpr (GATE)
+        if (j < mine) put<T, (W >= 4)>(at<T>(a.grad_gate, b, t0 + j, d), mul(z, slope[j]), left);
+    }
+    __syncthreads();
+
+    // 3. the gradients, backwards
+    V flow = leave[lane];
+    if (warp > 0) {
+      flow = fold(flow, Q, E);
+    } else {
+      for (int w = kWarps - 1; w > 0; --w) flow = fold(flow, agg_q[w][lane], agg_e[w][lane]);
+    }
+#pragma unroll
+    for (int j = S - 1; j >= 0; --j) {
+      const V G = add(dh[j], flow);
+      flow = fma(q[j], G, G);
+      V dx = G, df = mul(before[j], flow);
+      if (FORM == RET_SCAN_LOGIT) {
+        dx = scan::turn<FORM>(mul(q[j], G));
+        df = mul(mul(add(before[j], get<T>(f + kX + j * kPiece)), q[j]), flow);
       }
       if (j < mine) {
-        dx.template put<(W >= 4)>(at<T>(a.grad_x, b, t0 + j, d), left);
-        df.template put<(W >= 4)>(at<T>(a.grad_f, b, t0 + j, d), left);
+        put<T, (W >= 4)>(at<T>(a.grad_x, b, t0 + j, d), dx, left);
+        put<T, (W >= 4)>(at<T>(a.grad_f, b, t0 + j, d), df, left);
       }
     }
-    if (a.d_state_in && tile == 0 && warp == 0) {
-#pragma unroll
-      for (int i = 0; i < n; ++i)
-        if (i < left) a.d_state_in[(size_t)b * a.D + d + i] = flow[i];
-    }
+    if (a.d_state_in && tile == 0 && warp == 0)
+      put_state(a.d_state_in + (size_t)b * a.D + d, flow, left);
     if (threadIdx.x == 0) items.take[slot] = next;
     __syncthreads();
     load(slot);
@@ -620,19 +678,23 @@ __global__ void __launch_bounds__(kThreads) scan_token(const ScanArgs a) {
   const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
   if (i >= (long long)a.B * per_row) return;
   const long long b = i / per_row, d = (i - b * per_row) * V;
-  float h[V], f[V], x[V], g[V];
-  load_pack<float, V>(a.state_in + b * a.D + d, h);
-  load_pack<T, V>(at<T>(a.f, b, 0, d), f);
-  load_pack<T, V>(at<T>(a.x, b, 0, d), x);
+  Vec<V> z, f, x;
+  load_pack<float, V>(a.state_in + b * a.D + d, z.v);
+  load_pack<T, V>(at<T>(a.f, b, 0, d), f.v);
+  load_pack<T, V>(at<T>(a.x, b, 0, d), x.v);
+  float g[V];
   if constexpr (GATE) load_pack<T, V>(at<T>(a.gate, b, 0, d), g);
 #pragma unroll
-  for (int v = 0; v < V; ++v) h[v] = advance<FORM>(h[v], complement<FORM>(f[v]), x[v]);
-  store_pack<float, V>(a.state_out + b * a.D + d, h);
+  for (int v = 0; v < V; ++v) {
+    const Vec<1> q = less_one<FORM>(Vec<1>{{f.v[v]}});
+    z.v[v] = turn<FORM>(advance<FORM>(Vec<1>{{turn<FORM>(z.v[v])}}, q, Vec<1>{{x.v[v]}}).v[0]);
+  }
+  store_pack<float, V>(a.state_out + b * a.D + d, z.v);
   if constexpr (GATE) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] *= g[v] * sigmoidf(g[v]);
+    for (int v = 0; v < V; ++v) z.v[v] *= g[v] * sigmoidf(g[v]);
   }
-  store_pack<T, V>(at<T>(a.y, b, 0, d), h);
+  store_pack<T, V>(at<T>(a.y, b, 0, d), z.v);
 }
 
 // Calls fn with the element type, the form and whether there is a gate as
@@ -673,8 +735,8 @@ Plan plan(const ScanArgs& a, int tok) {
     char* ws = static_cast<char*>(a.workspace);
     const size_t n = words(a.B, a.D, a.dtype, p.tiles);
     p.ticket = reinterpret_cast<int*>(ws);
-    p.span = reinterpret_cast<float2*>(ws + kHead);
-    p.end = reinterpret_cast<float*>(ws + kHead + n * sizeof(float2));
+    p.span = reinterpret_cast<float*>(ws + kHead);
+    p.end = p.span + 2 * n;
   }
   return p;
 }
