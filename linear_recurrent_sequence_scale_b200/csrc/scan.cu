@@ -141,36 +141,51 @@ __device__ __forceinline__ T* at(const Operand& o, long long b, long long t, lon
 // next ones run while one is computed), and per item
 //   1. each of 8 warps scans its own kTok/8 tokens from zero, channels across
 //      lanes (4 bytes of them each), and leaves (Q, Z) in shared memory;
-//   2. warp 0 folds the eight, publishes the item's (Q, Z), looks back over
-//      the previous items of the same channels until it meets one whose end
-//      is published, folds forward from there, and publishes its own end;
-//   3. every warp runs its tokens again from the state that enters them and
-//      writes y.
+//   2. every warp folds the spans of the warps before it; the last one so has
+//      the item's (Q, Z) and publishes it;
+//   3. every warp runs its tokens again from the z that enters them and
+//      writes y; the last one publishes the item's end.
+// What enters the item is found meanwhile by a ninth warp, the scout: it looks
+// back over the previous items of the same channels until it meets one whose
+// end is published, and folds forward from there over the published spans.
 // So every element crosses HBM once, and neither few channels nor long
-// sequences leave SMs idle.
+// sequences leave SMs idle.  (With the look-back done by one of the eight
+// warps between 2 and 3, the others waited for it 60% of the time: 556 us
+// instead of 401 us for 65536 x 4096 in bf16.)
 //
-// Items are taken from a counter in time order: an item's predecessors are
-// held by blocks that already run, and each block works through its items in
-// the order it took them, so waiting for them always ends, whatever else the
-// GPU runs.  The wait is bounded in time all the same.  A published word is
+// Block k of G takes items k, k + G, k + 2 G ... of the order in time, and the
+// launch is cooperative: every block of it runs, or none, so an item's
+// predecessors are always being worked on and waiting for them ends, whatever
+// else the GPU runs.  The wait is bounded in time all the same.  (Items taken
+// from a counter instead, three ahead for the ring, end up in clumps: a block
+// that was held up takes its next ones in one burst, and its neighbours in
+// time then wait for one another: 651 us where this order takes 401.)  A
+// published word is
 // its own flag (every word of the workspace starts as kEmpty, which no
 // result of arithmetic is), so no fence or lock is needed, and folding from
 // any published end gives the same bits: the end of an item is itself the fold
 // of its (Q, Z) over the one before.
 constexpr int kWarps = 8;
-constexpr int kBlock = 32 * kWarps;
+constexpr int kCompute = 32 * kWarps;
+constexpr int kBlock = kCompute + 32;      // and the scout
 constexpr int kPiece = 128;                // bytes of one row of an item
 constexpr uint32_t kEmpty = 0xffffffffu;   // a NaN that arithmetic never returns
 constexpr int kWindow = 4;                 // predecessors looked at together
 constexpr int kSiteForward = 801, kSiteBackward = 802;
 
 struct Plan {
-  int* ticket;     // starts at -1 (all bits set, like the rest of the workspace)
   float* end;      // [tile][B][blocks][channels]: what leaves an item
   float* span;     // same, two words per channel: a lane's Q's, then its Z's
   int blocks;      // pieces of channels per batch row
+  int pieces;      // of all batch rows
   int tiles;       // items per piece
   int items;
+  // words from one turn to the next, and where a lane's begin (n channels per lane)
+  __device__ __forceinline__ size_t pitch(int n) const { return (size_t)pieces * 32 * n; }
+  template <typename Item>
+  __device__ __forceinline__ size_t words(const Item& it, int n, int lane) const {
+    return ((size_t)it.turn * pieces + it.rest) * 32 * n + lane * n;
+  }
 };
 
 __device__ __forceinline__ float word(float x) {
@@ -294,21 +309,28 @@ template <int N> __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// kTok rows of kPiece bytes: rows past `rows` and bytes past `bytes` become
+// TOK rows of kPiece bytes: rows past `rows` and bytes past `bytes` become
 // zeros.  W: bytes per access; 2 (rows aligned to a bf16 only) has no
 // asynchronous form and goes through registers.
 template <int W, int TOK>
 __device__ __forceinline__ void copy_item(char* dst, const char* src, long long pitch, int rows,
                                           int bytes) {
   if constexpr (W >= 4) {
-    constexpr int kPer = kPiece / W, kStep = kBlock / kPer;
-    const int col = (threadIdx.x % kPer) * W;
-    const uint32_t d = sm100::smem_u32(dst) + col;
+    constexpr int kPer = kPiece / W, kStep = kCompute / kPer;
+    const int col = (threadIdx.x % kPer) * W, r0 = threadIdx.x / kPer;
+    const uint32_t d = sm100::smem_u32(dst) + r0 * kPiece + col;
+    if (rows >= TOK && bytes >= kPiece) {
+      const char* s = src + r0 * pitch + col;
 #pragma unroll
-    for (int i = 0; i < TOK / kStep; ++i) {
-      const int r = i * kStep + threadIdx.x / kPer;
-      const bool ok = r < rows && col < bytes;
-      cp_async<W>(d + r * kPiece, ok ? src + r * pitch + col : src, ok);
+      for (int i = 0; i < TOK / kStep; ++i, s += kStep * pitch)
+        cp_async<W>(d + i * kStep * kPiece, s, true);
+    } else {
+#pragma unroll
+      for (int i = 0; i < TOK / kStep; ++i) {
+        const int r = i * kStep + r0;
+        const bool ok = r < rows && col < bytes;
+        cp_async<W>(d + i * kStep * kPiece, ok ? src + r * pitch + col : src, ok);
+      }
     }
   } else {
     const int col = (threadIdx.x % 32) * 4;
@@ -324,6 +346,11 @@ __device__ __forceinline__ void copy_item(char* dst, const char* src, long long 
       *reinterpret_cast<uint32_t*>(dst + r * kPiece + col) = v;
     }
   }
+}
+
+// Barrier of the eight computing warps.
+__device__ __forceinline__ void compute_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kCompute) : "memory");
 }
 
 // The channels of one lane: 4 bytes of a row.
@@ -366,9 +393,9 @@ template <int FORM, typename T>
 __device__ __forceinline__ void open_gates(char* f, int rows, int tok) {
   if (FORM == RET_SCAN_LOGIT && rows < tok) {
     const uint32_t inf = sizeof(T) == 2 ? 0x7f807f80u : 0x7f800000u;
-    for (int i = rows * (kPiece / 4) + threadIdx.x; i < tok * (kPiece / 4); i += kBlock)
+    for (int i = rows * (kPiece / 4) + threadIdx.x; i < tok * (kPiece / 4); i += kCompute)
       reinterpret_cast<uint32_t*>(f)[i] = inf;
-    __syncthreads();
+    compute_sync();
   }
 }
 
@@ -384,120 +411,182 @@ template <int OPERANDS, int TOK> struct Ring {
   static constexpr int kBytes = kStages * kStage;  // two blocks per SM
 };
 
-// Item bookkeeping shared by the two directions: slot s of the ring holds item
-// take[s]; one thread takes the next while the block computes.
-template <int STAGES> struct Items {
-  int take[STAGES];
+struct Item {
+  int turn;   // place in the order that state flows: 0 has no predecessor; -1: no item
+  int b;      // batch row
+  int block;  // piece of its channels
+  int rest;   // b and block in one
 };
+
+// What the scout hands to the computing warps: the block's items, STAGES ahead,
+// and what enters each.
+template <int STAGES, int n> struct Desk {
+  Item item[2 * STAGES];     // of round k: item[k % (2 STAGES)]
+  Vec<n> enter[2][32];       // of round k: enter[k % 2]
+  uint64_t full[2], free[2]; // barriers of enter
+};
+
+template <int STAGES, int n>
+__device__ __forceinline__ void take(Desk<STAGES, n>& desk, const Plan& p, int round) {
+  const int i = blockIdx.x + round * gridDim.x;
+  Item it = {-1, 0, 0, 0};
+  if (i < p.items) {
+    it.turn = i / p.pieces;
+    it.rest = i - it.turn * p.pieces;
+    it.b = it.rest / p.blocks;
+    it.block = it.rest - it.b * p.blocks;
+  }
+  desk.item[round % (2 * STAGES)] = it;
+}
+
+// By the whole block, before anything else: the first items and the barriers.
+template <int STAGES, int n>
+__device__ __forceinline__ void open_desk(Desk<STAGES, n>& desk, const Plan& p) {
+  if (threadIdx.x == kCompute) {
+    for (int s = 0; s < STAGES; ++s) take(desk, p, s);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      sm100::mbar_init(&desk.full[i], 1);
+      sm100::mbar_init(&desk.free[i], kWarps);
+    }
+    sm100::fence_mbar_init();
+  }
+  __syncthreads();
+}
+
+// The scout's rounds.  first(item): what enters a turn 0 item.
+template <int STAGES, int n, typename First>
+__device__ __forceinline__ void scout(Desk<STAGES, n>& desk, const Plan& p, int site,
+                                      First first) {
+  const int lane = threadIdx.x % 32;
+  for (int k = 0;; ++k) {
+    const Item it = desk.item[k % (2 * STAGES)];
+    if (it.turn < 0) return;
+    const Vec<n> z = it.turn > 0 ? look_back<n>(p, p.words(it, n, lane), p.pitch(n), it.turn, site)
+                                 : first(it);
+    // the slot's previous contents (round k - 2) have been read
+    if (k >= 2) sm100::mbar_wait(&desk.free[k % 2], (k / 2 - 1) % 2, site + 2);
+    desk.enter[k % 2][lane] = z;
+    if (lane == 0) take(desk, p, k + STAGES);
+    __syncwarp();
+    if (lane == 0) sm100::mbar_arrive(&desk.full[k % 2]);
+  }
+}
+
+// By the computing warps: what enters the item of round k.
+template <int STAGES, int n>
+__device__ __forceinline__ Vec<n> entering(Desk<STAGES, n>& desk, int k, int site) {
+  sm100::mbar_wait(&desk.full[k % 2], (k / 2) % 2, site + 4);
+  const int lane = threadIdx.x % 32;
+  const Vec<n> z = desk.enter[k % 2][lane];
+  __syncwarp();
+  if (lane == 0) sm100::mbar_arrive(&desk.free[k % 2]);
+  return z;
+}
 
 template <typename T, int FORM, bool GATE, int W>
 __global__ void __launch_bounds__(kBlock, 2) scan_items(const ScanArgs a, const Plan p) {
   using R = Ring<GATE ? 3 : 2, kTokForward>;
   constexpr int n = kLane<T>, kTok = kTokForward, S = kTok / kWarps, C = 32 * n;
+  constexpr int kX = R::kOperand, kGate = 2 * R::kOperand;
   using V = Vec<n>;
   extern __shared__ __align__(128) char ring[];
-  __shared__ Items<R::kStages> items;
-  __shared__ V agg_q[kWarps][32], agg_z[kWarps][32], enter[32];
+  __shared__ Desk<R::kStages, n> desk;
+  __shared__ V agg_q[kWarps][32], agg_z[kWarps][32];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const size_t pitch = (size_t)a.B * p.blocks * C;
-  const int pieces = a.B * p.blocks;
 
-  const auto load = [&](int slot) {
-    const int item = items.take[slot];
-    if (item < p.items) {
-      const int tile = item / pieces, rest = item - tile * pieces;
-      const int b = rest / p.blocks, d = (rest - b * p.blocks) * C;
-      const int t = tile * kTok, rows = a.N - t, bytes = (a.D - d) * (int)sizeof(T);
+  open_desk(desk, p);
+  if (warp == kWarps) {
+    scout(desk, p, kSiteForward, [&](const Item& it) {
+      const int d = it.block * C + lane * n;
+      return turn<FORM>(get_state<n>(
+          a.state_in ? a.state_in + (size_t)it.b * a.D + d : nullptr, a.D - d));
+    });
+    return;
+  }
+
+  const auto load = [&](int round, int slot) {
+    const Item it = desk.item[round % (2 * R::kStages)];
+    if (it.turn >= 0) {
+      const int t = it.turn * kTok, d = it.block * C;
+      const int rows = a.N - t, bytes = (a.D - d) * (int)sizeof(T);
       char* s = ring + slot * R::kStage;
-      copy_item<W, kTok>(s, (const char*)at<const T>(a.f, b, t, d), a.f.token * sizeof(T), rows,
+      copy_item<W, kTok>(s, (const char*)at<const T>(a.f, it.b, t, d), a.f.token * sizeof(T), rows,
                          bytes);
-      copy_item<W, kTok>(s + R::kOperand, (const char*)at<const T>(a.x, b, t, d),
+      copy_item<W, kTok>(s + kX, (const char*)at<const T>(a.x, it.b, t, d),
                          a.x.token * sizeof(T), rows, bytes);
       if constexpr (GATE)
-        copy_item<W, kTok>(s + 2 * R::kOperand, (const char*)at<const T>(a.gate, b, t, d),
+        copy_item<W, kTok>(s + kGate, (const char*)at<const T>(a.gate, it.b, t, d),
                            a.gate.token * sizeof(T), rows, bytes);
     }
     cp_commit();
   };
-
-  if (threadIdx.x == 0)
-    for (int s = 0; s < R::kStages; ++s)
-      items.take[s] = p.ticket ? atomicAdd(p.ticket, 1) + 1 : (int)(blockIdx.x + s * gridDim.x);
-  __syncthreads();
-  for (int s = 0; s < R::kStages; ++s) load(s);
+  for (int s = 0; s + 1 < R::kStages; ++s) load(s, s);
 
   for (int k = 0, slot = 0;; ++k, slot = slot + 1 == R::kStages ? 0 : slot + 1) {
-    const int item = items.take[slot];
-    if (item >= p.items) break;
-    const int tile = item / pieces, rest = item - tile * pieces;
-    const int b = rest / p.blocks, d0 = (rest - b * p.blocks) * C;
-    const int rows = min(kTok, a.N - tile * kTok);
-    const int d = d0 + lane * n, left = a.D - d;
-    const size_t words = (size_t)tile * pitch + (size_t)rest * C + lane * n;
-    int next = 0;
-    if (threadIdx.x == 0)
-      next = p.ticket ? atomicAdd(p.ticket, 1) + 1
-                      : (int)(blockIdx.x + (k + R::kStages) * gridDim.x);
-    cp_wait<R::kStages - 1>();
-    __syncthreads();
+    const Item it = desk.item[k % (2 * R::kStages)];
+    if (it.turn < 0) break;
+    const int b = it.b, d = it.block * C + lane * n, left = a.D - d;
+    const int rows = min(kTok, a.N - it.turn * kTok);
+    cp_wait<R::kStages - 2>();
+    compute_sync();  // the item is here, and the previous one's slot is free
+    load(k + R::kStages - 1, slot == 0 ? R::kStages - 1 : slot - 1);
     open_gates<FORM, T>(ring + slot * R::kStage, rows, kTok);
     const char* f = ring + slot * R::kStage + warp * S * kPiece;
-    const char* x = f + R::kOperand;
 
     // 1. this warp's tokens from zero
     V q[S], Q = all<n>(0.0f), Z = Q;
 #pragma unroll
     for (int j = 0; j < S; ++j) {
       q[j] = less_one<FORM>(get<T>(f + j * kPiece));
-      Z = advance<FORM>(Z, q[j], get<T>(x + j * kPiece));
+      Z = advance<FORM>(Z, q[j], get<T>(f + kX + j * kPiece));
       Q = chain(Q, q[j]);
     }
     agg_q[warp][lane] = Q;
     agg_z[warp][lane] = Z;
-    __syncthreads();
+    compute_sync();
 
-    // 2. what enters the item (warp 0), and the span of the warps before
-    Q = all<n>(0.0f), Z = Q;
-    for (int w = 0; w < (warp == 0 ? kWarps : warp); ++w) {
-      Z = fold(Z, agg_q[w][lane], agg_z[w][lane]);
-      Q = chain(Q, agg_q[w][lane]);
+    // 2. the span of the warps before, and of the item
+    V Qb = all<n>(0.0f), Zb = Qb;
+    for (int w = 0; w < warp; ++w) {
+      Zb = fold(Zb, agg_q[w][lane], agg_z[w][lane]);
+      Qb = chain(Qb, agg_q[w][lane]);
     }
-    V z;
-    if (warp == 0) {
-      if (tile > 0) {
-        if (tile + 1 < p.tiles) st_words(p.span + 2 * words, Q, Z);
-        z = look_back<n>(p, words, pitch, tile, kSiteForward);
-      } else {
-        z = turn<FORM>(get_state<n>(a.state_in ? a.state_in + (size_t)b * a.D + d : nullptr, left));
-      }
-      if (tile + 1 < p.tiles) st_words(p.end + words, fold(z, Q, Z));
-      enter[lane] = z;
+    const bool publish = warp == kWarps - 1 && it.turn + 1 < p.tiles;
+    const size_t words = p.words(it, n, lane);
+    if (publish) {
+      Z = fold(Zb, Q, Z);
+      Q = chain(Qb, Q);
+      st_words(p.span + 2 * words, Q, Z);
     }
-    __syncthreads();
+    V z = entering(desk, k, kSiteForward);
+    if (publish) st_words(p.end + words, fold(z, Q, Z));
+    z = fold(z, Qb, Zb);
 
     // 3. the same tokens from the z that enters them
-    if (warp > 0) z = fold(enter[lane], Q, Z);
-    const int t0 = tile * kTok + warp * S, mine = min(S, a.N - t0);
+    const int t0 = it.turn * kTok + warp * S, mine = min(S, a.N - t0);
     if (a.chunk_states && t0 % RET_SCAN_CHUNK == 0 && mine > 0)
       put_state(a.chunk_states +
                     ((size_t)b * cdiv(a.N, RET_SCAN_CHUNK) + t0 / RET_SCAN_CHUNK) * a.D + d,
                 turn<FORM>(z), left);
     T* y = at<T>(a.y, b, t0, d);
+    const auto token = [&](int j) {
+      z = advance<FORM>(z, q[j], get<T>(f + kX + j * kPiece));
+      V out = turn<FORM>(z);
+      if constexpr (GATE) out = mul(out, swish(get<T>(f + kGate + j * kPiece)));
+      put<T, (W >= 4)>(y, out, left);
+      y += a.y.token;
+    };
+    if (mine == S) {
 #pragma unroll
-    for (int j = 0; j < S; ++j) {
-      if (j < mine) {
-        z = advance<FORM>(z, q[j], get<T>(x + j * kPiece));
-        V out = turn<FORM>(z);
-        if constexpr (GATE) out = mul(out, swish(get<T>(f + 2 * R::kOperand + j * kPiece)));
-        put<T, (W >= 4)>(y, out, left);
-        y += a.y.token;
-      }
+      for (int j = 0; j < S; ++j) token(j);
+    } else {
+#pragma unroll
+      for (int j = 0; j < S; ++j)
+        if (j < mine) token(j);
     }
     if (a.state_out && mine > 0 && t0 + mine == a.N)
       put_state(a.state_out + (size_t)b * a.D + d, turn<FORM>(z), left);
-    if (threadIdx.x == 0) items.take[slot] = next;
-    __syncthreads();
-    load(slot);
   }
   cp_wait<0>();
 }
@@ -523,58 +612,55 @@ __global__ void __launch_bounds__(kBlock, 2) scan_items_backward(const ScanArgs 
   constexpr int kX = R::kOperand, kDy = 2 * R::kOperand, kGate = 3 * R::kOperand;
   constexpr int kState = (GATE ? 4 : 3) * R::kOperand;
   extern __shared__ __align__(128) char ring[];
-  __shared__ Items<R::kStages> items;
-  __shared__ V agg_q[kWarps][32], agg_z[kWarps][32], agg_e[kWarps][32], leave[32];
+  __shared__ Desk<R::kStages, n> desk;
+  __shared__ V agg_q[kWarps][32], agg_z[kWarps][32], agg_e[kWarps][32];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const size_t pitch = (size_t)a.B * p.blocks * C;
-  const int pieces = a.B * p.blocks;
 
-  const auto load = [&](int slot) {
-    const int item = items.take[slot];
-    if (item < p.items) {
-      const int turn = item / pieces, rest = item - turn * pieces, tile = p.tiles - 1 - turn;
-      const int b = rest / p.blocks, d = (rest - b * p.blocks) * C;
-      const int t = tile * kTok, rows = a.N - t, bytes = (a.D - d) * (int)sizeof(T);
+  open_desk(desk, p);
+  if (warp == kWarps) {
+    scout(desk, p, kSiteBackward, [&](const Item& it) {
+      const int d = it.block * C + lane * n;
+      return get_state<n>(a.d_state_out ? a.d_state_out + (size_t)it.b * a.D + d : nullptr,
+                          a.D - d);
+    });
+    return;
+  }
+
+  const auto load = [&](int round, int slot) {
+    const Item it = desk.item[round % (2 * R::kStages)];
+    if (it.turn >= 0) {
+      const int tile = p.tiles - 1 - it.turn, t = tile * kTok, d = it.block * C;
+      const int rows = a.N - t, bytes = (a.D - d) * (int)sizeof(T);
       char* s = ring + slot * R::kStage;
-      copy_item<W, kTok>(s, (const char*)at<const T>(a.f, b, t, d), a.f.token * sizeof(T), rows,
+      copy_item<W, kTok>(s, (const char*)at<const T>(a.f, it.b, t, d), a.f.token * sizeof(T), rows,
                          bytes);
-      copy_item<W, kTok>(s + kX, (const char*)at<const T>(a.x, b, t, d), a.x.token * sizeof(T),
-                         rows, bytes);
-      copy_item<W, kTok>(s + kDy, (const char*)at<const T>(a.d_y, b, t, d),
+      copy_item<W, kTok>(s + kX, (const char*)at<const T>(a.x, it.b, t, d),
+                         a.x.token * sizeof(T), rows, bytes);
+      copy_item<W, kTok>(s + kDy, (const char*)at<const T>(a.d_y, it.b, t, d),
                          a.d_y.token * sizeof(T), rows, bytes);
       if constexpr (GATE)
-        copy_item<W, kTok>(s + kGate, (const char*)at<const T>(a.gate, b, t, d),
+        copy_item<W, kTok>(s + kGate, (const char*)at<const T>(a.gate, it.b, t, d),
                            a.gate.token * sizeof(T), rows, bytes);
       if (threadIdx.x < C) {
         const bool ok = d + (int)threadIdx.x < a.D;
-        const float* st = a.chunk_states + ((size_t)b * p.tiles + tile) * a.D + d;
+        const float* st = a.chunk_states + ((size_t)it.b * p.tiles + tile) * a.D + d;
         cp_async<4>(sm100::smem_u32(s + kState) + threadIdx.x * 4,
                     (const char*)(st + (ok ? threadIdx.x : 0)), ok);
       }
     }
     cp_commit();
   };
-
-  if (threadIdx.x == 0)
-    for (int s = 0; s < R::kStages; ++s)
-      items.take[s] = p.ticket ? atomicAdd(p.ticket, 1) + 1 : (int)(blockIdx.x + s * gridDim.x);
-  __syncthreads();
-  for (int s = 0; s < R::kStages; ++s) load(s);
+  for (int s = 0; s + 1 < R::kStages; ++s) load(s, s);
 
   for (int k = 0, slot = 0;; ++k, slot = slot + 1 == R::kStages ? 0 : slot + 1) {
-    const int item = items.take[slot];
-    if (item >= p.items) break;
-    const int turn = item / pieces, rest = item - turn * pieces, tile = p.tiles - 1 - turn;
-    const int b = rest / p.blocks, d0 = (rest - b * p.blocks) * C;
+    const Item it = desk.item[k % (2 * R::kStages)];
+    if (it.turn < 0) break;
+    const int tile = p.tiles - 1 - it.turn;
+    const int b = it.b, d = it.block * C + lane * n, left = a.D - d;
     const int rows = min(kTok, a.N - tile * kTok);
-    const int d = d0 + lane * n, left = a.D - d;
-    const size_t words = (size_t)turn * pitch + (size_t)rest * C + lane * n;
-    int next = 0;
-    if (threadIdx.x == 0)
-      next = p.ticket ? atomicAdd(p.ticket, 1) + 1
-                      : (int)(blockIdx.x + (k + R::kStages) * gridDim.x);
-    cp_wait<R::kStages - 1>();
-    __syncthreads();
+    cp_wait<R::kStages - 2>();
+    compute_sync();
+    load(k + R::kStages - 1, slot == 0 ? R::kStages - 1 : slot - 1);
     const char* stage = ring + slot * R::kStage;
     open_gates<FORM, T>(ring + slot * R::kStage, rows, kTok);
     const char* f = stage + warp * S * kPiece;
@@ -591,7 +677,7 @@ __global__ void __launch_bounds__(kBlock, 2) scan_items_backward(const ScanArgs 
         const V g = get<T>(f + kGate + j * kPiece), sig = sigmoid(g), sw = mul(g, sig);
         // swish'(g) = sig + sw (1 - sig), with the sign of z
         const V rest = fma(sig, all<n>(-1.0f), all<n>(1.0f));
-        slope[j] = scan::turn<FORM>(mul(dh[j], fma(sw, rest, sig)));
+        slope[j] = turn<FORM>(mul(dh[j], fma(sw, rest, sig)));
         dh[j] = mul(dh[j], sw);
       }
     }
@@ -603,32 +689,27 @@ __global__ void __launch_bounds__(kBlock, 2) scan_items_backward(const ScanArgs 
     agg_q[warp][lane] = Q;
     agg_z[warp][lane] = Z;
     agg_e[warp][lane] = E;
-    __syncthreads();
+    compute_sync();
 
-    // 2. the flow that reaches the item from behind (warp 0), and the span of
-    // the warps behind
-    Q = all<n>(0.0f), E = Q;
-    for (int w = kWarps - 1; w >= (warp == 0 ? 0 : warp + 1); --w) {
-      E = fold(E, agg_q[w][lane], agg_e[w][lane]);
-      Q = chain(Q, agg_q[w][lane]);
+    // 2. the span of the warps behind, and of the item
+    V Qb = all<n>(0.0f), Eb = Qb;
+    for (int w = kWarps - 1; w > warp; --w) {
+      Eb = fold(Eb, agg_q[w][lane], agg_e[w][lane]);
+      Qb = chain(Qb, agg_q[w][lane]);
     }
-    if (warp == 0) {
-      V e;
-      if (turn > 0) {
-        if (turn + 1 < p.tiles) st_words(p.span + 2 * words, Q, E);
-        e = look_back<n>(p, words, pitch, turn, kSiteBackward);
-      } else {
-        e = get_state<n>(a.d_state_out ? a.d_state_out + (size_t)b * a.D + d : nullptr, left);
-      }
-      if (turn + 1 < p.tiles) st_words(p.end + words, fold(e, Q, E));
-      leave[lane] = e;
+    const bool publish = warp == 0 && it.turn + 1 < p.tiles;
+    const size_t words = p.words(it, n, lane);
+    if (publish) {
+      E = fold(Eb, Q, E);
+      Q = chain(Qb, Q);
+      st_words(p.span + 2 * words, Q, E);
     }
-    // meanwhile z forwards from the state that enters the chunk
+    // z forwards from the state that enters the chunk
     const int t0 = tile * kTok + warp * S, mine = min(S, a.N - t0);
     V z, before[S];
 #pragma unroll
     for (int i = 0; i < n; ++i)
-      z.v[i] = scan::turn<FORM>(reinterpret_cast<const float*>(stage + kState)[lane * n + i]);
+      z.v[i] = turn<FORM>(reinterpret_cast<const float*>(stage + kState)[lane * n + i]);
     for (int w = 0; w < warp; ++w) z = fold(z, agg_q[w][lane], agg_z[w][lane]);
 #pragma unroll
     for (int j = 0; j < S; ++j) {
@@ -637,22 +718,18 @@ __global__ void __launch_bounds__(kBlock, 2) scan_items_backward(const ScanArgs 
       if constexpr (GATE)
         if (j < mine) put<T, (W >= 4)>(at<T>(a.grad_gate, b, t0 + j, d), mul(z, slope[j]), left);
     }
-    __syncthreads();
 
     // 3. the gradients, backwards
-    V flow = leave[lane];
-    if (warp > 0) {
-      flow = fold(flow, Q, E);
-    } else {
-      for (int w = kWarps - 1; w > 0; --w) flow = fold(flow, agg_q[w][lane], agg_e[w][lane]);
-    }
+    V flow = entering(desk, k, kSiteBackward);
+    if (publish) st_words(p.end + words, fold(flow, Q, E));
+    flow = fold(flow, Qb, Eb);
 #pragma unroll
     for (int j = S - 1; j >= 0; --j) {
       const V G = add(dh[j], flow);
       flow = fma(q[j], G, G);
       V dx = G, df = mul(before[j], flow);
       if (FORM == RET_SCAN_LOGIT) {
-        dx = scan::turn<FORM>(mul(q[j], G));
+        dx = turn<FORM>(mul(q[j], G));
         df = mul(mul(add(before[j], get<T>(f + kX + j * kPiece)), q[j]), flow);
       }
       if (j < mine) {
@@ -662,9 +739,6 @@ __global__ void __launch_bounds__(kBlock, 2) scan_items_backward(const ScanArgs 
     }
     if (a.d_state_in && tile == 0 && warp == 0)
       put_state(a.d_state_in + (size_t)b * a.D + d, flow, left);
-    if (threadIdx.x == 0) items.take[slot] = next;
-    __syncthreads();
-    load(slot);
   }
   cp_wait<0>();
 }
@@ -715,8 +789,6 @@ cudaError_t dispatch(int dtype, int form, bool gate, Fn fn) {
 
 namespace scan {
 
-constexpr size_t kHead = 256;  // the ticket's place at the front of the workspace
-
 int channels_per_piece(int dtype) { return kPiece / (dtype == RET_BF16 ? 2 : 4); }
 
 // Words of one kind (end states; half of the spans) that `tiles` items per
@@ -730,12 +802,11 @@ Plan plan(const ScanArgs& a, int tok) {
   Plan p = {};
   p.blocks = cdiv(a.D, channels_per_piece(a.dtype));
   p.tiles = cdiv(a.N, tok);
-  p.items = a.B * p.blocks * p.tiles;
+  p.pieces = a.B * p.blocks;
+  p.items = p.pieces * p.tiles;
   if (p.tiles > 1) {
-    char* ws = static_cast<char*>(a.workspace);
     const size_t n = words(a.B, a.D, a.dtype, p.tiles);
-    p.ticket = reinterpret_cast<int*>(ws);
-    p.span = reinterpret_cast<float*>(ws + kHead);
+    p.span = static_cast<float*>(a.workspace);
     p.end = p.span + 2 * n;
   }
   return p;
@@ -756,17 +827,39 @@ int access(const ScanArgs& a) {
   return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
 }
 
+// Blocks of a kernel that fit on the current device at once.
+template <typename Kernel> cudaError_t resident(Kernel kernel, int smem, int* blocks) {
+  int dev = 0, per_sm = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess)
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kBlock, smem);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  *blocks = per_sm * sms;
+  return e != cudaSuccess || *blocks > 0 ? e : cudaErrorInvalidConfiguration;
+}
+
 template <typename Kernel>
 cudaError_t run(Kernel kernel, const ScanArgs& a, const Plan& p, int smem, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  int most = 0;
+  cudaError_t e = resident(kernel, smem, &most);
   if (e != cudaSuccess) return e;
-  if (p.ticket) {
-    const size_t bytes = kHead + 12 * words(a.B, a.D, a.dtype, p.tiles);
-    if ((e = cudaMemsetAsync(a.workspace, 0xff, bytes, st)) != cudaSuccess) return e;
+  const dim3 grid(p.items < most ? p.items : most);
+  if (p.tiles == 1) {  // nothing to wait for
+    kernel<<<grid, kBlock, smem, st>>>(a, p);
+    return cudaPeekAtLastError();
   }
-  const int most = 2 * sm_count();
-  kernel<<<p.items < most ? p.items : most, kBlock, smem, st>>>(a, p);
-  return cudaPeekAtLastError();
+  e = cudaMemsetAsync(a.workspace, 0xff, 12 * words(a.B, a.D, a.dtype, p.tiles), st);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid, cfg.blockDim = dim3(kBlock), cfg.dynamicSmemBytes = smem, cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeCooperative;
+  attr.val.cooperative = 1;
+  cfg.attrs = &attr, cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, a, p);
+  return e != cudaSuccess ? e : cudaPeekAtLastError();
 }
 
 }  // namespace scan
@@ -777,7 +870,7 @@ int scan_device_error() { return read_clear_device_error(); }
 // sequence of one item needs none.
 size_t scan_workspace_bytes(int B, int N, int D, int dtype) {
   const int tiles = cdiv(N, scan::kTokBackward);
-  return tiles > 1 ? scan::kHead + 12 * scan::words(B, D, dtype, tiles) : 0;
+  return tiles > 1 ? 12 * scan::words(B, D, dtype, tiles) : 0;
 }
 
 cudaError_t launch_scan(const ScanArgs& a, cudaStream_t st) {
