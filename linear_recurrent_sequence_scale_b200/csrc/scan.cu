@@ -20,9 +20,13 @@
 #include "kernels.h"
 #include "rowvec.cuh"
 #include "sm100.cuh"
+#include "tmap.h"
 
 namespace ret {
 namespace scan {
+
+template <typename T> struct Type { using type = T; };
+template <int I> struct Int { static constexpr int value = I; };
 
 // The n = 1 or 2 channels that a lane computes together; two go through the
 // paired float32 instructions, which hold the kernels' issue rate under what
@@ -167,7 +171,6 @@ __device__ __forceinline__ T* at(const Operand& o, long long b, long long t, lon
 // of its (Q, Z) over the one before.
 constexpr int kWarps = 8;
 constexpr int kCompute = 32 * kWarps;
-constexpr int kBlock = kCompute + 32;      // and the scout
 constexpr int kPiece = 128;                // bytes of one row of an item
 constexpr uint32_t kEmpty = 0xffffffffu;   // a NaN that arithmetic never returns
 constexpr int kWindow = 4;                 // predecessors looked at together
@@ -180,6 +183,8 @@ struct Plan {
   int pieces;      // of all batch rows
   int tiles;       // items per piece
   int items;
+  int skip_turns, skip_rest;  // from one of a block's items to its next: the grid
+                              // in whole turns, and the rest of it
   // words from one turn to the next, and where a lane's begin (n channels per lane)
   __device__ __forceinline__ size_t pitch(int n) const { return (size_t)pieces * 32 * n; }
   template <typename Item>
@@ -360,6 +365,9 @@ template <typename T> __device__ __forceinline__ Vec<kLane<T>> get(const char* r
   load_pack<T, kLane<T>>(reinterpret_cast<const T*>(row) + (threadIdx.x % 32) * kLane<T>, r.v);
   return r;
 }
+template <typename T, int n> __device__ __forceinline__ void set(char* row, const Vec<n>& x) {
+  store_pack<T, n>(reinterpret_cast<T*>(row) + (threadIdx.x % 32) * n, x.v);
+}
 // `left`: channels of the piece that exist from this lane's first one on.
 template <typename T, bool PAIR, int n>
 __device__ __forceinline__ void put(T* p, const Vec<n>& x, int left) {
@@ -387,17 +395,6 @@ template <int FORM, int n> __device__ __forceinline__ Vec<n> turn(Vec<n> h) {
   for (int i = 0; i < n; ++i) h.v[i] = turn<FORM>(h.v[i]);
   return h;
 }
-// Rows past the end of a sequence hold zeros, which is a decay of 1 and no
-// input for LOG; LOGIT needs its gate at +inf for that.
-template <int FORM, typename T>
-__device__ __forceinline__ void open_gates(char* f, int rows, int tok) {
-  if (FORM == RET_SCAN_LOGIT && rows < tok) {
-    const uint32_t inf = sizeof(T) == 2 ? 0x7f807f80u : 0x7f800000u;
-    for (int i = rows * (kPiece / 4) + threadIdx.x; i < tok * (kPiece / 4); i += kCompute)
-      reinterpret_cast<uint32_t*>(f)[i] = inf;
-    compute_sync();
-  }
-}
 
 constexpr int kTokForward = 128, kTokBackward = RET_SCAN_CHUNK;
 static_assert(kTokForward % RET_SCAN_CHUNK == 0, "chunk states are kept at warp boundaries");
@@ -406,68 +403,63 @@ static_assert((kTokForward / kWarps) * (RET_SCAN_CHUNK / (kTokForward / kWarps))
 
 template <int OPERANDS, int TOK> struct Ring {
   static constexpr int kOperand = TOK * kPiece;
-  static constexpr int kStage = OPERANDS * kOperand + 256;  // + one float per channel
-  static constexpr int kStages = kStage <= 36 * 1024 ? 3 : 2;
+  static constexpr int kStage = OPERANDS * kOperand;
+  static constexpr int kStages = kStage <= 32 * 1024 ? 3 : 2;
   static constexpr int kBytes = kStages * kStage;  // two blocks per SM
 };
 
-struct Item {
-  int turn;   // place in the order that state flows: 0 has no predecessor; -1: no item
-  int b;      // batch row
-  int block;  // piece of its channels
-  int rest;   // b and block in one
-};
-
-// What the scout hands to the computing warps: the block's items, STAGES ahead,
-// and what enters each.
-template <int STAGES, int n> struct Desk {
-  Item item[2 * STAGES];     // of round k: item[k % (2 STAGES)]
-  Vec<n> enter[2][32];       // of round k: enter[k % 2]
-  uint64_t full[2], free[2]; // barriers of enter
-};
-
-template <int STAGES, int n>
-__device__ __forceinline__ void take(Desk<STAGES, n>& desk, const Plan& p, int round) {
-  const int i = blockIdx.x + round * gridDim.x;
-  Item it = {-1, 0, 0, 0};
-  if (i < p.items) {
-    it.turn = i / p.pieces;
-    it.rest = i - it.turn * p.pieces;
-    it.b = it.rest / p.blocks;
-    it.block = it.rest - it.b * p.blocks;
+// The items of a block, one after another.
+struct Walk {
+  int turn;  // place in the order that state flows: 0 has no predecessor
+  int rest;  // batch row and piece of its channels in one
+  __device__ __forceinline__ Walk(const Plan& p)
+      : turn(blockIdx.x / p.pieces), rest(blockIdx.x % p.pieces) {}
+  __device__ __forceinline__ void next(const Plan& p) {
+    turn += p.skip_turns;
+    rest += p.skip_rest;
+    if (rest >= p.pieces) rest -= p.pieces, ++turn;
   }
-  desk.item[round % (2 * STAGES)] = it;
-}
+  __device__ __forceinline__ bool ends(const Plan& p) const { return turn >= p.tiles; }
+};
 
-// By the whole block, before anything else: the first items and the barriers.
-template <int STAGES, int n>
-__device__ __forceinline__ void open_desk(Desk<STAGES, n>& desk, const Plan& p) {
-  if (threadIdx.x == kCompute) {
-    for (int s = 0; s < STAGES; ++s) take(desk, p, s);
+// What the scout hands to the computing warps: what enters the item of round
+// k, in enter[k % 2]; and the ring's barriers where TMA fills and empties it.
+template <int STAGES, int n> struct Desk {
+  Vec<n> enter[2][32];
+  uint64_t full[2], free[2];
+  uint64_t loaded[STAGES], done[STAGES];
+};
+
+// By the whole block, before anything else.
+template <int STAGES, int n> __device__ __forceinline__ void open_desk(Desk<STAGES, n>& desk) {
+  if (threadIdx.x == 0) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       sm100::mbar_init(&desk.full[i], 1);
       sm100::mbar_init(&desk.free[i], kWarps);
+    }
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) {
+      sm100::mbar_init(&desk.loaded[i], 1);
+      sm100::mbar_init(&desk.done[i], kWarps);
     }
     sm100::fence_mbar_init();
   }
   __syncthreads();
 }
 
-// The scout's rounds.  first(item): what enters a turn 0 item.
+// The scout's rounds.  first(rest): what enters a turn 0 item.
 template <int STAGES, int n, typename First>
 __device__ __forceinline__ void scout(Desk<STAGES, n>& desk, const Plan& p, int site,
                                       First first) {
   const int lane = threadIdx.x % 32;
-  for (int k = 0;; ++k) {
-    const Item it = desk.item[k % (2 * STAGES)];
-    if (it.turn < 0) return;
-    const Vec<n> z = it.turn > 0 ? look_back<n>(p, p.words(it, n, lane), p.pitch(n), it.turn, site)
-                                 : first(it);
+  Walk w(p);
+  for (int k = 0; !w.ends(p); ++k, w.next(p)) {
+    const Vec<n> z = w.turn > 0 ? look_back<n>(p, p.words(w, n, lane), p.pitch(n), w.turn, site)
+                                : first(w.rest);
     // the slot's previous contents (round k - 2) have been read
     if (k >= 2) sm100::mbar_wait(&desk.free[k % 2], (k / 2 - 1) % 2, site + 2);
     desk.enter[k % 2][lane] = z;
-    if (lane == 0) take(desk, p, k + STAGES);
     __syncwarp();
     if (lane == 0) sm100::mbar_arrive(&desk.full[k % 2]);
   }
@@ -484,111 +476,224 @@ __device__ __forceinline__ Vec<n> entering(Desk<STAGES, n>& desk, int k, int sit
   return z;
 }
 
+// An operand as TMA sees it: [D] x the pitch that is smaller x the larger one.
+struct Mapped {
+  CUtensorMap map;
+  int time_major;  // the batch pitch is the smaller one
+};
+__device__ __forceinline__ void tma_load(void* dst, const Mapped& m, uint64_t* bar, int d, int t,
+                                         int b) {
+  sm100::tma_load_3d(dst, &m.map, bar, d, m.time_major ? b : t, m.time_major ? t : b);
+}
+__device__ __forceinline__ void tma_store(const Mapped& m, const void* src, int d, int t, int b) {
+  sm100::tma_store_3d(&m.map, sm100::smem_u32(src), d, m.time_major ? b : t,
+                      m.time_major ? t : b);
+}
+
+// One thread's rounds where TMA moves the items: operands 0 .. IN-1 of an item
+// are loaded to its slot, and once the computing warps have put results in
+// place of some of them, those are stored and the slot is filled again.  Rows
+// and channels past the end read as zeros and are not written.  tile(turn):
+// place in time.  out[i]: the operand whose place result i has taken.
+template <int IN, int OUT, int TOK, int STAGES, int n, typename Tile>
+__device__ __forceinline__ void mover(Desk<STAGES, n>& desk, char* ring, const Plan& p,
+                                      const Mapped* in, const Mapped* out, const int (&place)[OUT],
+                                      int site, Tile tile) {
+  using R = Ring<IN, TOK>;
+  constexpr int C = 32 * n;
+  Walk ahead(p), w(p);
+  int loads[STAGES];
+#pragma unroll
+  for (int s = 0; s < STAGES; ++s) loads[s] = 0;
+  const auto load = [&](int slot) {
+    const int b = ahead.rest / p.blocks, d = (ahead.rest - b * p.blocks) * C;
+    const int t = tile(ahead.turn) * TOK;
+    sm100::mbar_arrive_expect_tx(&desk.loaded[slot], R::kStage);
+#pragma unroll
+    for (int i = 0; i < IN; ++i)
+      tma_load(ring + slot * R::kStage + i * R::kOperand, in[i], &desk.loaded[slot], d, t, b);
+    ahead.next(p);
+  };
+#pragma unroll
+  for (int s = 0; s < STAGES; ++s)
+    if (!ahead.ends(p)) load(s), ++loads[s];
+  bool ok = true;
+  for (int k = 0; ok && !w.ends(p);) {
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s, ++k) {
+      if (!ok || w.ends(p)) break;
+      ok = sm100::mbar_wait(&desk.done[s], (k / STAGES) % 2, site + 6);
+      if (!ok) break;
+      const int b = w.rest / p.blocks, d = (w.rest - b * p.blocks) * C;
+      const int t = tile(w.turn) * TOK;
+#pragma unroll
+      for (int i = 0; i < OUT; ++i)
+        tma_store(out[i], ring + s * R::kStage + place[i] * R::kOperand, d, t, b);
+      sm100::bulk_commit();
+      w.next(p);
+      if (!ahead.ends(p)) {
+        sm100::bulk_wait_read0();
+        load(s), ++loads[s];
+      }
+    }
+  }
+  sm100::bulk_wait0();
+  if (!ok) {  // some wait gave up: the loads under way still end before the block does
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s) {
+      const uint64_t t0 = sm100::globaltimer();
+      while (loads[s] > 0 && !sm100::mbar_try_wait(&desk.loaded[s], (loads[s] - 1) % 2) &&
+             sm100::globaltimer() - t0 < sm100::kWaitLimitNs) {
+      }
+    }
+  }
+}
+
+// Threads of a block: the computing warps, the scout, and the mover.
+template <int W> constexpr int kBlockOf = kCompute + 32 + (W == 16 ? 32 : 0);
+
+template <int OPERANDS, int W> struct Maps {
+  Mapped m[OPERANDS];
+};
+template <int OPERANDS> struct Maps<OPERANDS, 4> {};
+template <int OPERANDS> struct Maps<OPERANDS, 2> {};
+
+// A token that is not there: a decay of 1 and, its x being zero, no input.
+template <int FORM, int n> __device__ __forceinline__ void mask(Vec<n>& q, bool there) {
+  if (FORM == RET_SCAN_LOGIT && !there) q = all<n>(0.0f);
+}
+
+// W: bytes that every row of every operand is aligned to (16, 4 or 2).  With
+// 16, TMA moves the items: the loads cost the computing warps nothing, and y
+// leaves from the place of f without an address or a bound being computed.
+// Otherwise the computing warps copy, and store y themselves.
 template <typename T, int FORM, bool GATE, int W>
-__global__ void __launch_bounds__(kBlock, 2) scan_items(const ScanArgs a, const Plan p) {
-  using R = Ring<GATE ? 3 : 2, kTokForward>;
+__global__ void __launch_bounds__(kBlockOf<W>, 2)
+scan_items(const ScanArgs a, const Plan p, const __grid_constant__ Maps<GATE ? 4 : 3, W> maps) {
+  constexpr int IN = GATE ? 3 : 2;  // f, x, gate
+  using R = Ring<IN, kTokForward>;
   constexpr int n = kLane<T>, kTok = kTokForward, S = kTok / kWarps, C = 32 * n;
-  constexpr int kX = R::kOperand, kGate = 2 * R::kOperand;
+  constexpr int ST = R::kStages, kX = R::kOperand, kGate = 2 * R::kOperand;
+  constexpr bool kTma = W == 16;
   using V = Vec<n>;
   extern __shared__ __align__(128) char ring[];
-  __shared__ Desk<R::kStages, n> desk;
-  __shared__ V agg_q[kWarps][32], agg_z[kWarps][32];
+  __shared__ Desk<ST, n> desk;
+  __shared__ V agg_q[2][kWarps][32], agg_z[2][kWarps][32];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
-  open_desk(desk, p);
+  open_desk(desk);
   if (warp == kWarps) {
-    scout(desk, p, kSiteForward, [&](const Item& it) {
-      const int d = it.block * C + lane * n;
-      return turn<FORM>(get_state<n>(
-          a.state_in ? a.state_in + (size_t)it.b * a.D + d : nullptr, a.D - d));
+    scout(desk, p, kSiteForward, [&](int rest) {
+      const int b = rest / p.blocks, d = (rest - b * p.blocks) * C + lane * n;
+      return turn<FORM>(
+          get_state<n>(a.state_in ? a.state_in + (size_t)b * a.D + d : nullptr, a.D - d));
     });
     return;
   }
+  if constexpr (kTma) {
+    if (warp > kWarps) {
+      if (lane == 0)
+        mover<IN, 1, kTok>(desk, ring, p, maps.m, maps.m + IN, {0}, kSiteForward,
+                           [](int turn) { return turn; });
+      return;
+    }
+  }
 
-  const auto load = [&](int round, int slot) {
-    const Item it = desk.item[round % (2 * R::kStages)];
-    if (it.turn >= 0) {
-      const int t = it.turn * kTok, d = it.block * C;
-      const int rows = a.N - t, bytes = (a.D - d) * (int)sizeof(T);
+  Walk ahead(p), w(p);
+  const auto load = [&](int slot) {
+    if (!ahead.ends(p)) {
+      const int b = ahead.rest / p.blocks, d = (ahead.rest - b * p.blocks) * C;
+      const int t = ahead.turn * kTok, rows = a.N - t, bytes = (a.D - d) * (int)sizeof(T);
       char* s = ring + slot * R::kStage;
-      copy_item<W, kTok>(s, (const char*)at<const T>(a.f, it.b, t, d), a.f.token * sizeof(T), rows,
+      copy_item<W, kTok>(s, (const char*)at<const T>(a.f, b, t, d), a.f.token * sizeof(T), rows,
                          bytes);
-      copy_item<W, kTok>(s + kX, (const char*)at<const T>(a.x, it.b, t, d),
-                         a.x.token * sizeof(T), rows, bytes);
+      copy_item<W, kTok>(s + kX, (const char*)at<const T>(a.x, b, t, d), a.x.token * sizeof(T),
+                         rows, bytes);
       if constexpr (GATE)
-        copy_item<W, kTok>(s + kGate, (const char*)at<const T>(a.gate, it.b, t, d),
+        copy_item<W, kTok>(s + kGate, (const char*)at<const T>(a.gate, b, t, d),
                            a.gate.token * sizeof(T), rows, bytes);
+      ahead.next(p);
     }
     cp_commit();
   };
-  for (int s = 0; s + 1 < R::kStages; ++s) load(s, s);
+  if constexpr (!kTma)
+    for (int s = 0; s + 1 < ST; ++s) load(s);
 
-  for (int k = 0, slot = 0;; ++k, slot = slot + 1 == R::kStages ? 0 : slot + 1) {
-    const Item it = desk.item[k % (2 * R::kStages)];
-    if (it.turn < 0) break;
-    const int b = it.b, d = it.block * C + lane * n, left = a.D - d;
-    const int rows = min(kTok, a.N - it.turn * kTok);
-    cp_wait<R::kStages - 2>();
-    compute_sync();  // the item is here, and the previous one's slot is free
-    load(k + R::kStages - 1, slot == 0 ? R::kStages - 1 : slot - 1);
-    open_gates<FORM, T>(ring + slot * R::kStage, rows, kTok);
-    const char* f = ring + slot * R::kStage + warp * S * kPiece;
+  for (int k = 0, slot = 0, phase = 0; !w.ends(p); ++k, w.next(p)) {
+    const int b = w.rest / p.blocks, d = (w.rest - b * p.blocks) * C + lane * n, left = a.D - d;
+    const int t0 = w.turn * kTok + warp * S, mine = min(S, a.N - t0);
+    if constexpr (kTma) {
+      sm100::mbar_wait(&desk.loaded[slot], phase, kSiteForward + 8);
+    } else {
+      cp_wait<ST - 2>();
+      compute_sync();  // the item is here, and the previous one's slot is free
+      load(slot == 0 ? ST - 1 : slot - 1);
+    }
+    char* f = ring + slot * R::kStage + warp * S * kPiece;
 
     // 1. this warp's tokens from zero
     V q[S], Q = all<n>(0.0f), Z = Q;
+    const auto from_zero = [&](auto whole) {
 #pragma unroll
-    for (int j = 0; j < S; ++j) {
-      q[j] = less_one<FORM>(get<T>(f + j * kPiece));
-      Z = advance<FORM>(Z, q[j], get<T>(f + kX + j * kPiece));
-      Q = chain(Q, q[j]);
-    }
-    agg_q[warp][lane] = Q;
-    agg_z[warp][lane] = Z;
+      for (int j = 0; j < S; ++j) {
+        q[j] = less_one<FORM>(get<T>(f + j * kPiece));
+        if (!decltype(whole)::value) mask<FORM>(q[j], j < mine);
+        Z = advance<FORM>(Z, q[j], get<T>(f + kX + j * kPiece));
+        Q = chain(Q, q[j]);
+      }
+    };
+    if (mine == S)
+      from_zero(Int<1>());
+    else
+      from_zero(Int<0>());
+    agg_q[k % 2][warp][lane] = Q;
+    agg_z[k % 2][warp][lane] = Z;
     compute_sync();
 
     // 2. the span of the warps before, and of the item
     V Qb = all<n>(0.0f), Zb = Qb;
-    for (int w = 0; w < warp; ++w) {
-      Zb = fold(Zb, agg_q[w][lane], agg_z[w][lane]);
-      Qb = chain(Qb, agg_q[w][lane]);
+    for (int v = 0; v < warp; ++v) {
+      Zb = fold(Zb, agg_q[k % 2][v][lane], agg_z[k % 2][v][lane]);
+      Qb = chain(Qb, agg_q[k % 2][v][lane]);
     }
-    const bool publish = warp == kWarps - 1 && it.turn + 1 < p.tiles;
-    const size_t words = p.words(it, n, lane);
+    const bool publish = warp == kWarps - 1 && w.turn + 1 < p.tiles;
     if (publish) {
       Z = fold(Zb, Q, Z);
       Q = chain(Qb, Q);
-      st_words(p.span + 2 * words, Q, Z);
+      st_words(p.span + 2 * p.words(w, n, lane), Q, Z);
     }
     V z = entering(desk, k, kSiteForward);
-    if (publish) st_words(p.end + words, fold(z, Q, Z));
+    if (publish) st_words(p.end + p.words(w, n, lane), fold(z, Q, Z));
     z = fold(z, Qb, Zb);
 
     // 3. the same tokens from the z that enters them
-    const int t0 = it.turn * kTok + warp * S, mine = min(S, a.N - t0);
     if (a.chunk_states && t0 % RET_SCAN_CHUNK == 0 && mine > 0)
       put_state(a.chunk_states +
                     ((size_t)b * cdiv(a.N, RET_SCAN_CHUNK) + t0 / RET_SCAN_CHUNK) * a.D + d,
                 turn<FORM>(z), left);
-    T* y = at<T>(a.y, b, t0, d);
-    const auto token = [&](int j) {
+    T* y = kTma ? nullptr : at<T>(a.y, b, t0, d);
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
       z = advance<FORM>(z, q[j], get<T>(f + kX + j * kPiece));
       V out = turn<FORM>(z);
       if constexpr (GATE) out = mul(out, swish(get<T>(f + kGate + j * kPiece)));
-      put<T, (W >= 4)>(y, out, left);
-      y += a.y.token;
-    };
-    if (mine == S) {
-#pragma unroll
-      for (int j = 0; j < S; ++j) token(j);
-    } else {
-#pragma unroll
-      for (int j = 0; j < S; ++j)
-        if (j < mine) token(j);
+      if constexpr (kTma) {
+        set<T>(f + j * kPiece, out);
+      } else {
+        if (j < mine) put<T, (W >= 4)>(y, out, left);
+        y += a.y.token;
+      }
     }
     if (a.state_out && mine > 0 && t0 + mine == a.N)
       put_state(a.state_out + (size_t)b * a.D + d, turn<FORM>(z), left);
+    if constexpr (kTma) {
+      sm100::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(&desk.done[slot]);
+    }
+    if (++slot == ST) slot = 0, phase ^= 1;
   }
-  cp_wait<0>();
+  if constexpr (!kTma) cp_wait<0>();
 }
 
 // Backward.  With G_t the gradient that reaches h_t from y_t and from
@@ -605,123 +710,142 @@ __global__ void __launch_bounds__(kBlock, 2) scan_items(const ScanArgs a, const 
 // forward call, h is recomputed in float32 inside it, and the flow is looked
 // for in the items after it as the forward does in those before.
 template <typename T, int FORM, bool GATE, int W>
-__global__ void __launch_bounds__(kBlock, 2) scan_items_backward(const ScanArgs a, const Plan p) {
-  using R = Ring<GATE ? 4 : 3, kTokBackward>;
+__global__ void __launch_bounds__(kBlockOf<W>, 2)
+scan_items_backward(const ScanArgs a, const Plan p,
+                    const __grid_constant__ Maps<GATE ? 7 : 5, W> maps) {
+  constexpr int IN = GATE ? 4 : 3;  // f, x, d_y, gate; grad_f, grad_x and grad_gate in their place
+  using R = Ring<IN, kTokBackward>;
   constexpr int n = kLane<T>, kTok = kTokBackward, S = kTok / kWarps, C = 32 * n;
+  constexpr int ST = R::kStages, kX = R::kOperand, kDy = 2 * R::kOperand, kGate = 3 * R::kOperand;
+  constexpr bool kTma = W == 16;
   using V = Vec<n>;
-  constexpr int kX = R::kOperand, kDy = 2 * R::kOperand, kGate = 3 * R::kOperand;
-  constexpr int kState = (GATE ? 4 : 3) * R::kOperand;
   extern __shared__ __align__(128) char ring[];
-  __shared__ Desk<R::kStages, n> desk;
-  __shared__ V agg_q[kWarps][32], agg_z[kWarps][32], agg_e[kWarps][32];
+  __shared__ Desk<ST, n> desk;
+  __shared__ V agg_q[2][kWarps][32], agg_z[2][kWarps][32], agg_e[2][kWarps][32];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
-  open_desk(desk, p);
+  open_desk(desk);
   if (warp == kWarps) {
-    scout(desk, p, kSiteBackward, [&](const Item& it) {
-      const int d = it.block * C + lane * n;
-      return get_state<n>(a.d_state_out ? a.d_state_out + (size_t)it.b * a.D + d : nullptr,
-                          a.D - d);
+    scout(desk, p, kSiteBackward, [&](int rest) {
+      const int b = rest / p.blocks, d = (rest - b * p.blocks) * C + lane * n;
+      return get_state<n>(a.d_state_out ? a.d_state_out + (size_t)b * a.D + d : nullptr, a.D - d);
     });
     return;
   }
+  if constexpr (kTma) {
+    if (warp > kWarps) {
+      const auto tile = [&](int turn) { return p.tiles - 1 - turn; };
+      if (lane == 0) {
+        if constexpr (GATE)
+          mover<IN, 3, kTok>(desk, ring, p, maps.m, maps.m + IN, {0, 1, 3}, kSiteBackward, tile);
+        else
+          mover<IN, 2, kTok>(desk, ring, p, maps.m, maps.m + IN, {0, 1}, kSiteBackward, tile);
+      }
+      return;
+    }
+  }
 
-  const auto load = [&](int round, int slot) {
-    const Item it = desk.item[round % (2 * R::kStages)];
-    if (it.turn >= 0) {
-      const int tile = p.tiles - 1 - it.turn, t = tile * kTok, d = it.block * C;
+  Walk ahead(p), w(p);
+  const auto load = [&](int slot) {
+    if (!ahead.ends(p)) {
+      const int b = ahead.rest / p.blocks, d = (ahead.rest - b * p.blocks) * C;
+      const int t = (p.tiles - 1 - ahead.turn) * kTok;
       const int rows = a.N - t, bytes = (a.D - d) * (int)sizeof(T);
       char* s = ring + slot * R::kStage;
-      copy_item<W, kTok>(s, (const char*)at<const T>(a.f, it.b, t, d), a.f.token * sizeof(T), rows,
+      copy_item<W, kTok>(s, (const char*)at<const T>(a.f, b, t, d), a.f.token * sizeof(T), rows,
                          bytes);
-      copy_item<W, kTok>(s + kX, (const char*)at<const T>(a.x, it.b, t, d),
-                         a.x.token * sizeof(T), rows, bytes);
-      copy_item<W, kTok>(s + kDy, (const char*)at<const T>(a.d_y, it.b, t, d),
+      copy_item<W, kTok>(s + kX, (const char*)at<const T>(a.x, b, t, d), a.x.token * sizeof(T),
+                         rows, bytes);
+      copy_item<W, kTok>(s + kDy, (const char*)at<const T>(a.d_y, b, t, d),
                          a.d_y.token * sizeof(T), rows, bytes);
       if constexpr (GATE)
-        copy_item<W, kTok>(s + kGate, (const char*)at<const T>(a.gate, it.b, t, d),
+        copy_item<W, kTok>(s + kGate, (const char*)at<const T>(a.gate, b, t, d),
                            a.gate.token * sizeof(T), rows, bytes);
-      if (threadIdx.x < C) {
-        const bool ok = d + (int)threadIdx.x < a.D;
-        const float* st = a.chunk_states + ((size_t)it.b * p.tiles + tile) * a.D + d;
-        cp_async<4>(sm100::smem_u32(s + kState) + threadIdx.x * 4,
-                    (const char*)(st + (ok ? threadIdx.x : 0)), ok);
-      }
+      ahead.next(p);
     }
     cp_commit();
   };
-  for (int s = 0; s + 1 < R::kStages; ++s) load(s, s);
+  if constexpr (!kTma)
+    for (int s = 0; s + 1 < ST; ++s) load(s);
 
-  for (int k = 0, slot = 0;; ++k, slot = slot + 1 == R::kStages ? 0 : slot + 1) {
-    const Item it = desk.item[k % (2 * R::kStages)];
-    if (it.turn < 0) break;
-    const int tile = p.tiles - 1 - it.turn;
-    const int b = it.b, d = it.block * C + lane * n, left = a.D - d;
-    const int rows = min(kTok, a.N - tile * kTok);
-    cp_wait<R::kStages - 2>();
-    compute_sync();
-    load(k + R::kStages - 1, slot == 0 ? R::kStages - 1 : slot - 1);
-    const char* stage = ring + slot * R::kStage;
-    open_gates<FORM, T>(ring + slot * R::kStage, rows, kTok);
-    const char* f = stage + warp * S * kPiece;
+  for (int k = 0, slot = 0, phase = 0; !w.ends(p); ++k, w.next(p)) {
+    const int b = w.rest / p.blocks, d = (w.rest - b * p.blocks) * C + lane * n, left = a.D - d;
+    const int tile = p.tiles - 1 - w.turn, t0 = tile * kTok + warp * S, mine = min(S, a.N - t0);
+    // what enters the chunk: read here, needed after 1
+    V z = get_state<n>(a.chunk_states + ((size_t)b * p.tiles + tile) * a.D + d, left);
+    if constexpr (kTma) {
+      sm100::mbar_wait(&desk.loaded[slot], phase, kSiteBackward + 8);
+    } else {
+      cp_wait<ST - 2>();
+      compute_sync();
+      load(slot == 0 ? ST - 1 : slot - 1);
+    }
+    char* f = ring + slot * R::kStage + warp * S * kPiece;
 
     // 1. this warp's tokens: forwards from a zero state, backwards from a zero flow
     V q[S], dh[S], slope[GATE ? S : 1], Q = all<n>(0.0f), Z = Q, E = Q;
+    const auto from_zero = [&](auto whole) {
 #pragma unroll
-    for (int j = 0; j < S; ++j) {
-      q[j] = less_one<FORM>(get<T>(f + j * kPiece));
-      Z = advance<FORM>(Z, q[j], get<T>(f + kX + j * kPiece));
-      Q = chain(Q, q[j]);
-      dh[j] = get<T>(f + kDy + j * kPiece);
-      if constexpr (GATE) {
-        const V g = get<T>(f + kGate + j * kPiece), sig = sigmoid(g), sw = mul(g, sig);
-        // swish'(g) = sig + sw (1 - sig), with the sign of z
-        const V rest = fma(sig, all<n>(-1.0f), all<n>(1.0f));
-        slope[j] = turn<FORM>(mul(dh[j], fma(sw, rest, sig)));
-        dh[j] = mul(dh[j], sw);
+      for (int j = 0; j < S; ++j) {
+        q[j] = less_one<FORM>(get<T>(f + j * kPiece));
+        if (!decltype(whole)::value) mask<FORM>(q[j], j < mine);
+        Z = advance<FORM>(Z, q[j], get<T>(f + kX + j * kPiece));
+        Q = chain(Q, q[j]);
+        dh[j] = get<T>(f + kDy + j * kPiece);
+        if constexpr (GATE) {
+          const V g = get<T>(f + kGate + j * kPiece), sig = sigmoid(g), sw = mul(g, sig);
+          // swish'(g) = sig + sw (1 - sig), with the sign of z
+          const V rest = fma(sig, all<n>(-1.0f), all<n>(1.0f));
+          slope[j] = turn<FORM>(mul(dh[j], fma(sw, rest, sig)));
+          dh[j] = mul(dh[j], sw);
+        }
       }
-    }
+    };
+    if (mine == S)
+      from_zero(Int<1>());
+    else
+      from_zero(Int<0>());
 #pragma unroll
     for (int j = S - 1; j >= 0; --j) {
       const V G = add(dh[j], E);
       E = fma(q[j], G, G);
     }
-    agg_q[warp][lane] = Q;
-    agg_z[warp][lane] = Z;
-    agg_e[warp][lane] = E;
+    agg_q[k % 2][warp][lane] = Q;
+    agg_z[k % 2][warp][lane] = Z;
+    agg_e[k % 2][warp][lane] = E;
     compute_sync();
 
     // 2. the span of the warps behind, and of the item
     V Qb = all<n>(0.0f), Eb = Qb;
-    for (int w = kWarps - 1; w > warp; --w) {
-      Eb = fold(Eb, agg_q[w][lane], agg_e[w][lane]);
-      Qb = chain(Qb, agg_q[w][lane]);
+    for (int v = kWarps - 1; v > warp; --v) {
+      Eb = fold(Eb, agg_q[k % 2][v][lane], agg_e[k % 2][v][lane]);
+      Qb = chain(Qb, agg_q[k % 2][v][lane]);
     }
-    const bool publish = warp == 0 && it.turn + 1 < p.tiles;
-    const size_t words = p.words(it, n, lane);
+    const bool publish = warp == 0 && w.turn + 1 < p.tiles;
     if (publish) {
       E = fold(Eb, Q, E);
       Q = chain(Qb, Q);
-      st_words(p.span + 2 * words, Q, E);
+      st_words(p.span + 2 * p.words(w, n, lane), Q, E);
     }
     // z forwards from the state that enters the chunk
-    const int t0 = tile * kTok + warp * S, mine = min(S, a.N - t0);
-    V z, before[S];
-#pragma unroll
-    for (int i = 0; i < n; ++i)
-      z.v[i] = turn<FORM>(reinterpret_cast<const float*>(stage + kState)[lane * n + i]);
-    for (int w = 0; w < warp; ++w) z = fold(z, agg_q[w][lane], agg_z[w][lane]);
+    z = turn<FORM>(z);
+    for (int v = 0; v < warp; ++v) z = fold(z, agg_q[k % 2][v][lane], agg_z[k % 2][v][lane]);
+    V before[S];
 #pragma unroll
     for (int j = 0; j < S; ++j) {
       before[j] = z;
       z = advance<FORM>(z, q[j], get<T>(f + kX + j * kPiece));
-      if constexpr (GATE)
-        if (j < mine) put<T, (W >= 4)>(at<T>(a.grad_gate, b, t0 + j, d), mul(z, slope[j]), left);
+      if constexpr (GATE) {
+        if constexpr (kTma)
+          set<T>(f + kGate + j * kPiece, mul(z, slope[j]));
+        else if (j < mine)
+          put<T, (W >= 4)>(at<T>(a.grad_gate, b, t0 + j, d), mul(z, slope[j]), left);
+      }
     }
 
     // 3. the gradients, backwards
     V flow = entering(desk, k, kSiteBackward);
-    if (publish) st_words(p.end + words, fold(flow, Q, E));
+    if (publish) st_words(p.end + p.words(w, n, lane), fold(flow, Q, E));
     flow = fold(flow, Qb, Eb);
 #pragma unroll
     for (int j = S - 1; j >= 0; --j) {
@@ -732,15 +856,24 @@ __global__ void __launch_bounds__(kBlock, 2) scan_items_backward(const ScanArgs 
         dx = turn<FORM>(mul(q[j], G));
         df = mul(mul(add(before[j], get<T>(f + kX + j * kPiece)), q[j]), flow);
       }
-      if (j < mine) {
+      if constexpr (kTma) {
+        set<T>(f + kX + j * kPiece, dx);
+        set<T>(f + j * kPiece, df);
+      } else if (j < mine) {
         put<T, (W >= 4)>(at<T>(a.grad_x, b, t0 + j, d), dx, left);
         put<T, (W >= 4)>(at<T>(a.grad_f, b, t0 + j, d), df, left);
       }
     }
     if (a.d_state_in && tile == 0 && warp == 0)
       put_state(a.d_state_in + (size_t)b * a.D + d, flow, left);
+    if constexpr (kTma) {
+      sm100::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(&desk.done[slot]);
+    }
+    if (++slot == ST) slot = 0, phase ^= 1;
   }
-  cp_wait<0>();
+  if constexpr (!kTma) cp_wait<0>();
 }
 
 // One token: h = a h + ..., y = h or swish(g) h.  A thread owns V channels of
@@ -773,8 +906,6 @@ __global__ void __launch_bounds__(kThreads) scan_token(const ScanArgs a) {
 
 // Calls fn with the element type, the form and whether there is a gate as
 // compile-time values.
-template <typename T> struct Type { using type = T; };
-template <int I> struct Int { static constexpr int value = I; };
 template <typename Fn>
 cudaError_t dispatch(int dtype, int form, bool gate, Fn fn) {
   auto with_form = [&](auto t) {
@@ -812,54 +943,111 @@ Plan plan(const ScanArgs& a, int tok) {
   return p;
 }
 
-// Bytes per access of the loads: what every row of every operand is aligned
-// to.  Stores take a lane's 4 bytes at once from 4 on.
-int access(const ScanArgs& a) {
+// Whether TMA can move an operand: 16-byte aligned rows, and pitches that its
+// maps can hold.
+bool mappable(const Operand& o, const ScanArgs& a, int es) {
+  const uint64_t row = (uint64_t)a.D * es, token = a.N > 1 ? (uint64_t)o.token * es : row;
+  const uint64_t batch = a.B > 1 ? (uint64_t)o.batch * es : token;
+  const uint64_t small = token < batch ? token : batch, large = token < batch ? batch : token;
+  return aligned_to(o.p, 16) && (row | token | batch) % 16 == 0 && large < ((uint64_t)1 << 40) &&
+         large % small == 0;
+}
+
+// What every row of every operand is aligned to, up to TMA's needs.
+int alignment(const ScanArgs& a) {
   const int es = a.dtype == RET_BF16 ? 2 : 4;
-  size_t bits = (size_t)a.D * es;
+  uint64_t bits = (uint64_t)a.D * es;
+  bool all = true;
   for (const Operand* o :
        {&a.x, &a.f, &a.gate, &a.y, &a.d_y, &a.grad_x, &a.grad_f, &a.grad_gate}) {
     if (!o->p) continue;
-    bits |= reinterpret_cast<size_t>(o->p);
-    if (a.B > 1) bits |= (size_t)o->batch * es;
-    if (a.N > 1) bits |= (size_t)o->token * es;
+    bits |= reinterpret_cast<uint64_t>(o->p);
+    if (a.B > 1) bits |= (uint64_t)o->batch * es;
+    if (a.N > 1) bits |= (uint64_t)o->token * es;
+    all = all && mappable(*o, a, es);
   }
-  return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
+  return all ? 16 : bits % 4 == 0 ? 4 : 2;
+}
+
+cudaError_t map_operand(Mapped* m, const Operand& o, const ScanArgs& a, int tok) {
+  const int es = a.dtype == RET_BF16 ? 2 : 4;
+  const uint64_t row = (uint64_t)a.D * es, token = a.N > 1 ? (uint64_t)o.token * es : row;
+  const uint64_t batch = a.B > 1 ? (uint64_t)o.batch * es : token;
+  m->time_major = batch < token;
+  const uint32_t box = kPiece / es;
+  return m->time_major
+             ? make_tmap_rows(&m->map, o.p, es, a.D, a.B, a.N, batch, token, box, 1, tok)
+             : make_tmap_rows(&m->map, o.p, es, a.D, a.N, a.B, token, batch, box, tok, 1);
 }
 
 // Blocks of a kernel that fit on the current device at once.
-template <typename Kernel> cudaError_t resident(Kernel kernel, int smem, int* blocks) {
+template <typename Kernel>
+cudaError_t resident(Kernel kernel, int threads, int smem, int* blocks) {
   int dev = 0, per_sm = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess)
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kBlock, smem);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   *blocks = per_sm * sms;
   return e != cudaSuccess || *blocks > 0 ? e : cudaErrorInvalidConfiguration;
 }
 
-template <typename Kernel>
-cudaError_t run(Kernel kernel, const ScanArgs& a, const Plan& p, int smem, cudaStream_t st) {
+// tok: tokens of an item; ops: the kernel's operands in the order of its maps.
+template <int W, int OPERANDS>
+cudaError_t run(void (*kernel)(ScanArgs, Plan, Maps<OPERANDS, W>), const ScanArgs& a, int tok,
+                int smem, const Operand* const (&ops)[OPERANDS], cudaStream_t st) {
   int most = 0;
-  cudaError_t e = resident(kernel, smem, &most);
+  cudaError_t e = resident(kernel, kBlockOf<W>, smem, &most);
   if (e != cudaSuccess) return e;
-  const dim3 grid(p.items < most ? p.items : most);
+  Plan p = plan(a, tok);
+  const int grid = p.items < most ? p.items : most;
+  p.skip_turns = grid / p.pieces, p.skip_rest = grid % p.pieces;
+  Maps<OPERANDS, W> maps;
+  if constexpr (W == 16)
+    for (int i = 0; i < OPERANDS; ++i)
+      if ((e = map_operand(&maps.m[i], *ops[i], a, tok)) != cudaSuccess) return e;
   if (p.tiles == 1) {  // nothing to wait for
-    kernel<<<grid, kBlock, smem, st>>>(a, p);
+    kernel<<<grid, kBlockOf<W>, smem, st>>>(a, p, maps);
     return cudaPeekAtLastError();
   }
   e = cudaMemsetAsync(a.workspace, 0xff, 12 * words(a.B, a.D, a.dtype, p.tiles), st);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid, cfg.blockDim = dim3(kBlock), cfg.dynamicSmemBytes = smem, cfg.stream = st;
+  cfg.gridDim = dim3(grid), cfg.blockDim = dim3(kBlockOf<W>);
+  cfg.dynamicSmemBytes = smem, cfg.stream = st;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeCooperative;
   attr.val.cooperative = 1;
   cfg.attrs = &attr, cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, a, p);
+  e = cudaLaunchKernelEx(&cfg, kernel, a, p, maps);
   return e != cudaSuccess ? e : cudaPeekAtLastError();
+}
+
+template <typename T, int F, bool G, int W>
+cudaError_t forward(const ScanArgs& a, cudaStream_t st) {
+  constexpr int smem = Ring<G ? 3 : 2, kTokForward>::kBytes;
+  if constexpr (G) {
+    const Operand* const ops[] = {&a.f, &a.x, &a.gate, &a.y};
+    return run<W>(scan_items<T, F, G, W>, a, kTokForward, smem, ops, st);
+  } else {
+    const Operand* const ops[] = {&a.f, &a.x, &a.y};
+    return run<W>(scan_items<T, F, G, W>, a, kTokForward, smem, ops, st);
+  }
+}
+
+template <typename T, int F, bool G, int W>
+cudaError_t backward(const ScanArgs& a, cudaStream_t st) {
+  constexpr int smem = Ring<G ? 4 : 3, kTokBackward>::kBytes;
+  if constexpr (G) {
+    const Operand* const ops[] = {&a.f,      &a.x,      &a.d_y,      &a.gate,
+                                  &a.grad_f, &a.grad_x, &a.grad_gate};
+    return run<W>(scan_items_backward<T, F, G, W>, a, kTokBackward, smem, ops, st);
+  } else {
+    const Operand* const ops[] = {&a.f, &a.x, &a.d_y, &a.grad_f, &a.grad_x};
+    return run<W>(scan_items_backward<T, F, G, W>, a, kTokBackward, smem, ops, st);
+  }
 }
 
 }  // namespace scan
@@ -874,35 +1062,28 @@ size_t scan_workspace_bytes(int B, int N, int D, int dtype) {
 }
 
 cudaError_t launch_scan(const ScanArgs& a, cudaStream_t st) {
-  const scan::Plan p = scan::plan(a, scan::kTokForward);
-  const int w = scan::access(a);
+  const int w = scan::alignment(a);
   return scan::dispatch(a.dtype, a.form, a.gate.p != nullptr, [&](auto t, auto form, auto gate) {
     using T = typename decltype(t)::type;
     constexpr int F = decltype(form)::value;
     constexpr bool G = decltype(gate)::value != 0;
-    constexpr int smem = scan::Ring<G ? 3 : 2, scan::kTokForward>::kBytes;
-    if (w == 16) return scan::run(scan::scan_items<T, F, G, 16>, a, p, smem, st);
-    if (sizeof(T) == 4 || w == 4) return scan::run(scan::scan_items<T, F, G, 4>, a, p, smem, st);
+    if (w == 16) return scan::forward<T, F, G, 16>(a, st);
     if constexpr (sizeof(T) == 2)
-      return scan::run(scan::scan_items<T, F, G, 2>, a, p, smem, st);
-    return cudaErrorInvalidValue;
+      if (w == 2) return scan::forward<T, F, G, 2>(a, st);
+    return scan::forward<T, F, G, 4>(a, st);
   });
 }
 
 cudaError_t launch_scan_backward(const ScanArgs& a, cudaStream_t st) {
-  const scan::Plan p = scan::plan(a, scan::kTokBackward);
-  const int w = scan::access(a);
+  const int w = scan::alignment(a);
   return scan::dispatch(a.dtype, a.form, a.gate.p != nullptr, [&](auto t, auto form, auto gate) {
     using T = typename decltype(t)::type;
     constexpr int F = decltype(form)::value;
     constexpr bool G = decltype(gate)::value != 0;
-    constexpr int smem = scan::Ring<G ? 4 : 3, scan::kTokBackward>::kBytes;
-    if (w == 16) return scan::run(scan::scan_items_backward<T, F, G, 16>, a, p, smem, st);
-    if (sizeof(T) == 4 || w == 4)
-      return scan::run(scan::scan_items_backward<T, F, G, 4>, a, p, smem, st);
+    if (w == 16) return scan::backward<T, F, G, 16>(a, st);
     if constexpr (sizeof(T) == 2)
-      return scan::run(scan::scan_items_backward<T, F, G, 2>, a, p, smem, st);
-    return cudaErrorInvalidValue;
+      if (w == 2) return scan::backward<T, F, G, 2>(a, st);
+    return scan::backward<T, F, G, 4>(a, st);
   });
 }
 
