@@ -59,105 +59,63 @@ template <typename T, int V, int CH, int TPR> struct Geo {
   static_assert(TPR <= 32 || kThreads == TPR, "the block barrier serves one row");
 };
 
-template <typename G> struct Row {
+template <typename G>
+struct Row : RowPart<typename G::type, G::kV, G::kCH, G::kTPR> {
   static constexpr int V = G::kV, CH = G::kCH, TPR = G::kTPR;
-  using T = typename G::type;
-  float v[CH][V];
-  template <typename S>  // elements past d read as zero
-  __device__ __forceinline__ void load(const S* p, int lane, int nv) {
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int i = c * TPR + lane;
-      if (i < nv) {
-        load_pack<S, V>(p + (long long)i * V, v[c]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < V; ++k) v[c][k] = 0.0f;
-      }
-    }
-  }
-  __device__ __forceinline__ void store(T* p, int lane, int nv) const {
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int i = c * TPR + lane;
-      if (i < nv) store_pack<T, V>(p + (long long)i * V, v[c]);
-    }
-  }
+  using Base = RowPart<typename G::type, V, CH, TPR>;
+  using Base::P;
+  using Base::v;
   // v <- v (.) w
   __device__ __forceinline__ void scale(const float* w, int lane, int nv) {
+    constexpr int Q = V < 4 ? V : 4;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int i = c * TPR + lane;
       if (i < nv) {
-        constexpr int P = V < 4 ? V : 4;
 #pragma unroll
-        for (int j = 0; j < V; j += P) {
-          float f[P];
-          load_pack<float, P>(w + (long long)i * V + j, f);
+        for (int j = 0; j < V; j += Q) {
+          float f[Q];
+          load_pack<float, Q>(w + (long long)i * V + j, f);
 #pragma unroll
-          for (int k = 0; k < P; ++k) v[c][j + k] *= f[k];
+          for (int k = 0; k < Q; ++k) v[c * V + j + k] *= f[k];
         }
       }
     }
   }
-  // v <- v + a (.) b for a row that exists (nv > 0)
-  __device__ __forceinline__ void add_product(const Row& a, const Row& b, int lane, int nv) {
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-      if (c * TPR + lane < nv) {
-#pragma unroll
-        for (int k = 0; k < V; ++k) v[c][k] = fmaf(a.v[c][k], b.v[c][k], v[c][k]);
-      }
-  }
-  // v <- N(v); returns r.  Elements past d stay zero.
-  __device__ __forceinline__ float normalise(int lane, int nv, bool layer, float eps, float inv_d,
-                                             float2* slots) {
-    if (layer) {
-      float s = 0.0f;
-#pragma unroll
-      for (int c = 0; c < CH; ++c)
-#pragma unroll
-        for (int k = 0; k < V; ++k) s += v[c][k];
-      const float mean = row_sum<TPR>(s, slots) * inv_d;
-#pragma unroll
-      for (int c = 0; c < CH; ++c)
-        if (c * TPR + lane < nv) {
-#pragma unroll
-          for (int k = 0; k < V; ++k) v[c][k] -= mean;
-        }
-    }
-    float q = 0.0f;
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int k = 0; k < V; ++k) q = fmaf(v[c][k], v[c][k], q);
-    const float r = rsqrtf(fmaf(row_sum<TPR>(q, slots + 32), inv_d, eps));
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int k = 0; k < V; ++k) v[c][k] *= r;
-    return r;
+  // v <- N(v); returns r.  slots: two of row_sum2's
+  __device__ __forceinline__ float norm(int lane, int nv, bool layer, float eps, float inv_d,
+                                        float2* slots) {
+    return this->normalise(lane, nv, layer, eps, inv_d, [&](float x, int which) {
+      return row_sum<TPR>(x, slots + 32 * which);
+    });
   }
   // v <- r (v - [mean(v)] - h mean(v (.) h)), the norm's backward
   __device__ __forceinline__ void norm_backward(const Row& h, float r, int lane, int nv, bool layer,
                                                 float inv_d, float2* slot) {
-    float s1 = 0.0f, s2 = 0.0f;
+    Vec<2> p1 = all<2>(0.0f), p2 = p1;
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        s1 += v[c][k];
-        s2 = fmaf(v[c][k], h.v[c][k], s2);
-      }
+    for (int i = 0; i < P; ++i) {
+      p1 = add(p1, pair(v, i));
+      p2 = fma(pair(v, i), pair(h.v, i), p2);
+    }
+    float s1 = total(p1), s2 = total(p2);
     row_sum2<TPR>(s1, s2, slot);
-    s1 = layer ? s1 * inv_d : 0.0f;
-    s2 *= inv_d;
+    s1 = layer ? s1 * -inv_d : 0.0f;
+    s2 *= -inv_d;
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
-      if (c * TPR + lane < nv) {
+    for (int i = 0; i < P; ++i)
+      set_pair(v, i,
+               mul(all<2>(r), fma(pair(h.v, i), all<2>(s2), add(pair(v, i), all<2>(s1)))));
+    if (layer) this->clear_rest(lane, nv);
+  }
+  // v <- v + a (.) b
+  __device__ __forceinline__ void add_product(const Row& a, const Row& b) {
 #pragma unroll
-        for (int k = 0; k < V; ++k) v[c][k] = r * (v[c][k] - s1 - h.v[c][k] * s2);
-      }
+    for (int i = 0; i < P; ++i) set_pair(v, i, fma(pair(a.v, i), pair(b.v, i), pair(v, i)));
+  }
+  __device__ __forceinline__ void times(float f) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) set_pair(v, i, mul(pair(v, i), all<2>(f)));
   }
 };
 
@@ -165,25 +123,27 @@ template <typename G>
 __global__ void __launch_bounds__(G::kThreads)
 add_norm_rows(AddNormArgs a) {
   using T = typename G::type;
+  using R = Row<G>;
   __shared__ float2 slots[4 * 32];
   const int lane = threadIdx.x % G::kTPR, nv = a.d / G::kV;
   const long long n = (long long)blockIdx.x * G::kRows + threadIdx.x / G::kTPR;
   const int take = n < a.rows ? nv : 0;  // threads past the last row only join the sums
   const long long at = min(n, a.rows - 1) * a.d;
   const float inv_d = 1.0f / a.d;
-  Row<G> u, s;
+  R u, s;
   u.load(static_cast<const T*>(a.x) + at, lane, take);
   if (a.residual) s.load(static_cast<const T*>(a.residual) + at, lane, take);
   if (a.post_norm != RET_NORM_NONE)
-    u.normalise(lane, take, a.post_norm == RET_NORM_LAYER, a.eps, inv_d, slots);
+    u.norm(lane, take, a.post_norm == RET_NORM_LAYER, a.eps, inv_d, slots);
   if (a.w_post) u.scale(a.w_post, lane, take);
+  u.times(a.beta);
+  if (a.residual) {
 #pragma unroll
-  for (int c = 0; c < G::kCH; ++c)
-#pragma unroll
-    for (int k = 0; k < G::kV; ++k)
-      u.v[c][k] = a.residual ? fmaf(a.alpha, s.v[c][k], a.beta * u.v[c][k]) : a.beta * u.v[c][k];
+    for (int i = 0; i < R::P; ++i)
+      set_pair(u.v, i, fma(all<2>(a.alpha), pair(s.v, i), pair(u.v, i)));
+  }
   u.store(static_cast<T*>(a.res_out) + at, lane, take);
-  u.normalise(lane, take, a.norm == RET_NORM_LAYER, a.eps, inv_d, slots + 64);
+  u.norm(lane, take, a.norm == RET_NORM_LAYER, a.eps, inv_d, slots + 64);
   if (a.w) u.scale(a.w, lane, take);
   u.store(static_cast<T*>(a.y) + at, lane, take);
 }
@@ -194,50 +154,42 @@ template <typename G>
 __global__ void __launch_bounds__(G::kThreads)
 add_norm_rows_backward(AddNormArgs a, float* part_w, float* part_post) {
   using T = typename G::type;
+  using R = Row<G>;
   __shared__ float2 slots[6 * 32];
   const int lane = threadIdx.x % G::kTPR, nv = a.d / G::kV;
   const float inv_d = 1.0f / a.d;
   const bool need_x = a.post_norm != RET_NORM_NONE || part_post;
-  Row<G> acc_w, acc_post;
+  R acc_w, acc_post;
 #pragma unroll
-  for (int c = 0; c < G::kCH; ++c)
-#pragma unroll
-    for (int k = 0; k < G::kV; ++k) acc_w.v[c][k] = acc_post.v[c][k] = 0.0f;
+  for (int i = 0; i < R::E; ++i) acc_w.v[i] = acc_post.v[i] = 0.0f;
   const long long groups = (a.rows + G::kRows - 1) / G::kRows;
   for (long long g = blockIdx.x; g < groups; g += gridDim.x) {
     const long long n = g * G::kRows + threadIdx.x / G::kTPR;
     const int take = n < a.rows ? nv : 0;
     const long long at = min(n, a.rows - 1) * a.d;
-    Row<G> h, d, s, x;
+    R h, d, s, x;
     h.load(static_cast<const T*>(a.res_out) + at, lane, take);
     d.load(static_cast<const T*>(a.d_y) + at, lane, take);
     if (a.d_res_out) s.load(static_cast<const T*>(a.d_res_out) + at, lane, take);
     if (need_x) x.load(static_cast<const T*>(a.x) + at, lane, take);
-    const float r = h.normalise(lane, take, a.norm == RET_NORM_LAYER, a.eps, inv_d, slots);
-    if (part_w) acc_w.add_product(d, h, lane, take);
+    const float r = h.norm(lane, take, a.norm == RET_NORM_LAYER, a.eps, inv_d, slots);
+    if (part_w) acc_w.add_product(d, h);
     if (a.w) d.scale(a.w, lane, take);
     d.norm_backward(h, r, lane, take, a.norm == RET_NORM_LAYER, inv_d, slots + 64);
     if (a.d_res_out) {
 #pragma unroll
-      for (int c = 0; c < G::kCH; ++c)
-#pragma unroll
-        for (int k = 0; k < G::kV; ++k) d.v[c][k] += s.v[c][k];
+      for (int i = 0; i < R::P; ++i) set_pair(d.v, i, add(pair(d.v, i), pair(s.v, i)));
     }
     if (a.grad_residual) {
-#pragma unroll
-      for (int c = 0; c < G::kCH; ++c)
-#pragma unroll
-        for (int k = 0; k < G::kV; ++k) s.v[c][k] = a.alpha * d.v[c][k];
+      s = d;
+      s.times(a.alpha);
       s.store(static_cast<T*>(a.grad_residual) + at, lane, take);
     }
-#pragma unroll
-    for (int c = 0; c < G::kCH; ++c)
-#pragma unroll
-      for (int k = 0; k < G::kV; ++k) d.v[c][k] *= a.beta;
+    d.times(a.beta);
     float rx = 1.0f;
     if (a.post_norm != RET_NORM_NONE)
-      rx = x.normalise(lane, take, a.post_norm == RET_NORM_LAYER, a.eps, inv_d, slots + 96);
-    if (part_post) acc_post.add_product(d, x, lane, take);
+      rx = x.norm(lane, take, a.post_norm == RET_NORM_LAYER, a.eps, inv_d, slots + 96);
+    if (part_post) acc_post.add_product(d, x);
     if (a.grad_x) {
       if (a.w_post) d.scale(a.w_post, lane, take);
       if (a.post_norm != RET_NORM_NONE)
@@ -253,8 +205,8 @@ add_norm_rows_backward(AddNormArgs a, float* part_w, float* part_post) {
     if (i >= nv) continue;
 #pragma unroll
     for (int k = 0; k < G::kV; ++k) {
-      if (part_w) part_w[part + (long long)i * G::kV + k] = acc_w.v[c][k];
-      if (part_post) part_post[part + (long long)i * G::kV + k] = acc_post.v[c][k];
+      if (part_w) part_w[part + (long long)i * G::kV + k] = acc_w.v[c * G::kV + k];
+      if (part_post) part_post[part + (long long)i * G::kV + k] = acc_post.v[c * G::kV + k];
     }
   }
 }

@@ -691,6 +691,8 @@ int check_norm_gate(int B, int H, int N, int dv, int norm, float eps, int token_
   if (B < 1 || H < 1 || N < 0 || dv < 8 || dv % 8 || !valid_dtype(dtype)) return RET_EINVAL;
   if (!norm_kind(norm) || !(eps >= 0.0f) || isinf(eps)) return RET_EINVAL;
   if (dv > 1024 || (int64_t)B * H > 65535) return RET_EUNSUPPORTED;
+  // blocks of at least eight rows are counted in an int
+  if ((int64_t)B * H * (((int64_t)N + 7) / 8) > INT32_MAX) return RET_EUNSUPPORTED;
   if ((int64_t)B * H * N * dv > ((int64_t)1 << 40)) return RET_EUNSUPPORTED;
   const int64_t dense = (int64_t)H * dv;
   for (int i = 0; i < n_pitches; ++i) {

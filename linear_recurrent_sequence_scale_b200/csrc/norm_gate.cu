@@ -32,66 +32,30 @@ template <int TPR> __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-// Where row n of (batch, head) bh begins: head-major, or token-major with ld
-// elements between tokens.
-__device__ __forceinline__ long long row_at(int bh, int n, int H, int N, int dv, bool token_major,
-                                            long long ld) {
-  if (!token_major) return ((long long)bh * N + n) * dv;
-  const int b = bh / H;
-  return ((long long)b * N + n) * ld + (long long)(bh - b * H) * dv;
-}
-
-template <typename T, int CH, int TPR, bool GATE>
-struct Row {
-  static constexpr int V = 16 / sizeof(T);
-  float v[CH][V];
-  // elements past dv read as zero, so that they add nothing to a sum
-  __device__ __forceinline__ void load(const T* p, int lane, int nv) {
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int i = c * TPR + lane;
-      if (i < nv) {
-        load_pack<T, V>(p + (long long)i * V, v[c]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < V; ++k) v[c][k] = 0.0f;
-      }
-    }
+// The rows of a block: kTurns times kThreads / TPR tokens of one (batch, head).
+// Heads run fastest over the grid, so that the blocks at work together cover
+// whole tokens of the token-major arrays: with tokens fastest they would all
+// be in one head and touch one piece of d_v elements in every H (8 x 16 x 8192
+// x 512 in bf16: 656 against 641 us).  Several turns share the block's place
+// in the arrays, whose computation would otherwise cost as much as a row.
+constexpr int kTurns = 4;
+struct Where {
+  int b, h, n0;
+  __device__ __forceinline__ Where(int H, int N, int rows) {
+    const int blocks = cdiv(N, rows);
+    const unsigned rest = blockIdx.x / H;
+    h = blockIdx.x - rest * H;
+    b = rest / blocks;
+    n0 = (rest - b * blocks) * rows;
   }
-  __device__ __forceinline__ void store(T* p, int lane, int nv) const {
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int i = c * TPR + lane;
-      if (i < nv) store_pack<T, V>(p + (long long)i * V, v[c]);
-    }
+  // Where row n begins: head-major, or token-major with ld elements between tokens.
+  __device__ __forceinline__ long long head_major(int n, int H, int N, int dv) const {
+    return (((long long)b * H + h) * N + n) * dv;
   }
-  // v <- z, the normalised row; returns r.  Elements past dv stay zero.
-  __device__ __forceinline__ float normalise(int lane, int nv, bool layer, float eps, float inv_d) {
-    if (layer) {
-      float s = 0.0f;
-#pragma unroll
-      for (int c = 0; c < CH; ++c)
-#pragma unroll
-        for (int k = 0; k < V; ++k) s += v[c][k];
-      const float mean = row_sum<TPR>(s) * inv_d;
-#pragma unroll
-      for (int c = 0; c < CH; ++c)
-        if (c * TPR + lane < nv) {
-#pragma unroll
-          for (int k = 0; k < V; ++k) v[c][k] -= mean;
-        }
-    }
-    float q = 0.0f;
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int k = 0; k < V; ++k) q = fmaf(v[c][k], v[c][k], q);
-    const float r = rsqrtf(fmaf(row_sum<TPR>(q), inv_d, eps));
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int k = 0; k < V; ++k) v[c][k] *= r;
-    return r;
+  __device__ __forceinline__ long long at(int n, int H, int N, int dv, bool token_major,
+                                          long long ld) const {
+    return token_major ? ((long long)b * N + n) * ld + (long long)h * dv
+                       : head_major(n, H, N, dv);
   }
 };
 
@@ -99,23 +63,32 @@ template <typename T, int CH, int TPR, bool GATE>
 __global__ void __launch_bounds__(kThreads)
 norm_gate_rows(const T* y, const T* gate, T* o, int H, int N, int dv, bool layer, float eps,
                bool token_major, long long ldg, long long ldo) {
-  using R = Row<T, CH, TPR, GATE>;
-  constexpr int V = R::V;
-  const int lane = threadIdx.x % TPR, bh = blockIdx.y, nv = dv / V;
-  const int n = blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
-  const int take = n < N ? nv : 0;  // threads past the last row take part in the shuffles only
-  const int row = min(n, N - 1);
-  R z, g;
-  z.load(y + ((long long)bh * N + row) * dv, lane, take);
-  if constexpr (GATE) g.load(gate + row_at(bh, row, H, N, dv, token_major, ldg), lane, take);
-  z.normalise(lane, take, layer, eps, 1.0f / dv);
-  if constexpr (GATE) {
+  using R = RowPart<T, 16 / sizeof(T), CH, TPR>;
+  constexpr int kRows = kThreads / TPR;
+  const Where w(H, N, kTurns * kRows);
+  const int lane = threadIdx.x % TPR, nv = dv / (16 / (int)sizeof(T));
+  const float inv_d = 1.0f / dv;
+  int n = w.n0 + threadIdx.x / TPR;
+  y += w.head_major(n, H, N, dv);
+  if constexpr (GATE) gate += w.at(n, H, N, dv, token_major, ldg);
+  o += w.at(n, H, N, dv, token_major, ldo);
+  const long long step = (long long)kRows * dv, step_g = token_major ? kRows * ldg : step,
+                  step_o = token_major ? kRows * ldo : step;
+#pragma unroll 1
+  for (int i = 0; i < kTurns && w.n0 + i * kRows < N; ++i, n += kRows) {
+    const int take = n < N ? nv : 0;  // threads past the last row only join the shuffles
+    R z, g;
+    z.load(y, lane, take);
+    if constexpr (GATE) g.load(gate, lane, take);
+    z.normalise(lane, take, layer, eps, inv_d, [](float x, int) { return row_sum<TPR>(x); });
+    if constexpr (GATE) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int k = 0; k < V; ++k) z.v[c][k] *= g.v[c][k] * sigmoidf(g.v[c][k]);
+      for (int k = 0; k < R::P; ++k) set_pair(z.v, k, mul(pair(z.v, k), swish(pair(g.v, k))));
+    }
+    z.store(o, lane, take);
+    y += step, o += step_o;
+    if constexpr (GATE) gate += step_g;
   }
-  z.store(o + row_at(bh, row, H, N, dv, token_major, ldo), lane, take);
 }
 
 template <typename T, int CH, int TPR, bool GATE>
@@ -123,51 +96,66 @@ __global__ void __launch_bounds__(kThreads)
 norm_gate_rows_backward(const T* y, const T* gate, const T* d_o, T* grad_y, T* grad_gate, int H,
                         int N, int dv, bool layer, float eps, bool token_major, long long ldg,
                         long long lddo, long long ldgg) {
-  using R = Row<T, CH, TPR, GATE>;
-  constexpr int V = R::V;
-  const int lane = threadIdx.x % TPR, bh = blockIdx.y, nv = dv / V;
-  const int n = blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
-  const int take = n < N ? nv : 0;
-  const int row = min(n, N - 1);
+  using R = RowPart<T, 16 / sizeof(T), CH, TPR>;
+  constexpr int kRows = kThreads / TPR;
+  const Where w(H, N, kTurns * kRows);
+  const int lane = threadIdx.x % TPR, nv = dv / (16 / (int)sizeof(T));
   const float inv_d = 1.0f / dv;
-  R z, g, d;
-  z.load(y + ((long long)bh * N + row) * dv, lane, take);
-  d.load(d_o + row_at(bh, row, H, N, dv, token_major, lddo), lane, take);
-  if constexpr (GATE) g.load(gate + row_at(bh, row, H, N, dv, token_major, ldg), lane, take);
-  const float r = z.normalise(lane, take, layer, eps, inv_d);
-  float s1 = 0.0f, s2 = 0.0f;
+  int n = w.n0 + threadIdx.x / TPR;
+  y += w.head_major(n, H, N, dv);
+  grad_y += w.head_major(n, H, N, dv);
+  d_o += w.at(n, H, N, dv, token_major, lddo);
+  if constexpr (GATE) {
+    gate += w.at(n, H, N, dv, token_major, ldg);
+    grad_gate += w.at(n, H, N, dv, token_major, ldgg);
+  }
+  const long long step = (long long)kRows * dv, step_g = token_major ? kRows * ldg : step,
+                  step_o = token_major ? kRows * lddo : step,
+                  step_gg = token_major ? kRows * ldgg : step;
+#pragma unroll 1
+  for (int i = 0; i < kTurns && w.n0 + i * kRows < N; ++i, n += kRows) {
+    const int take = n < N ? nv : 0;
+    R z, g, d;
+    z.load(y, lane, take);
+    d.load(d_o, lane, take);
+    if constexpr (GATE) g.load(gate, lane, take);
+    const float r = z.normalise(lane, take, layer, eps, inv_d,
+                                [](float x, int) { return row_sum<TPR>(x); });
+    Vec<2> p1 = all<2>(0.0f), p2 = p1;
 #pragma unroll
-  for (int c = 0; c < CH; ++c)
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
+    for (int k = 0; k < R::P; ++k) {
+      Vec<2> dk = pair(d.v, k);
+      const Vec<2> zk = pair(z.v, k);
       if constexpr (GATE) {
-        float sw, slope;
-        swish_grad(g.v[c][k], &sw, &slope);
-        g.v[c][k] = d.v[c][k] * z.v[c][k] * slope;
-        d.v[c][k] *= sw;
+        Vec<2> sw, slope;
+        swish_grad(pair(g.v, k), &sw, &slope);
+        set_pair(g.v, k, mul(mul(dk, zk), slope));
+        dk = mul(dk, sw);
+        set_pair(d.v, k, dk);
       }
-      s1 += d.v[c][k];
-      s2 = fmaf(d.v[c][k], z.v[c][k], s2);
+      p1 = add(p1, dk);
+      p2 = fma(dk, zk, p2);
     }
-  if constexpr (GATE) g.store(grad_gate + row_at(bh, row, H, N, dv, token_major, ldgg), lane, take);
-  s1 = layer ? row_sum<TPR>(s1) * inv_d : 0.0f;
-  s2 = row_sum<TPR>(s2) * inv_d;
+    if constexpr (GATE) g.store(grad_gate, lane, take);
+    const float s1 = layer ? row_sum<TPR>(total(p1)) * -inv_d : 0.0f;
+    const float s2 = row_sum<TPR>(total(p2)) * -inv_d;
 #pragma unroll
-  for (int c = 0; c < CH; ++c)
-#pragma unroll
-    for (int k = 0; k < V; ++k) z.v[c][k] = r * (d.v[c][k] - s1 - z.v[c][k] * s2);
-  z.store(grad_y + ((long long)bh * N + row) * dv, lane, take);
+    for (int k = 0; k < R::P; ++k)
+      set_pair(z.v, k,
+               mul(all<2>(r), fma(pair(z.v, k), all<2>(s2), add(pair(d.v, k), all<2>(s1)))));
+    z.store(grad_y, lane, take);
+    y += step, grad_y += step, d_o += step_o;
+    if constexpr (GATE) gate += step_g, grad_gate += step_gg;
+  }
 }
 
-template <int I> struct Int { static constexpr int value = I; };
-
-// The fewest lanes whose 16-byte accesses cover a row; rows longer than a
-// warp's take more accesses per lane.
+// Two 16-byte accesses per lane and tensor, so that a row's sums cost few
+// shuffles per element (8 x 8 x 2048 x 256 backward: 74 us with one access
+// and twice the lanes, 65 with two); rows longer than a warp's take more.
 template <typename Fn> cudaError_t by_width(int nv, Fn fn) {
-  if (nv <= 4) return fn(Int<1>(), Int<4>());
-  if (nv <= 8) return fn(Int<1>(), Int<8>());
-  if (nv <= 16) return fn(Int<1>(), Int<16>());
-  if (nv <= 32) return fn(Int<1>(), Int<32>());
+  if (nv <= 8) return fn(Int<2>(), Int<4>());
+  if (nv <= 16) return fn(Int<2>(), Int<8>());
+  if (nv <= 32) return fn(Int<2>(), Int<16>());
   if (nv <= 64) return fn(Int<2>(), Int<32>());
   if (nv <= 128) return fn(Int<4>(), Int<32>());
   return fn(Int<8>(), Int<32>());
@@ -176,7 +164,7 @@ template <typename Fn> cudaError_t by_width(int nv, Fn fn) {
 template <typename T, bool GATE> cudaError_t forward_t(const NormGateArgs& a, cudaStream_t st) {
   return by_width(a.dv * (int)sizeof(T) / 16, [&](auto ch, auto tpr) {
     constexpr int CH = decltype(ch)::value, TPR = decltype(tpr)::value;
-    const dim3 grid(cdiv(a.N, kThreads / TPR), a.B * a.H);
+    const unsigned grid = (unsigned)cdiv(a.N, kTurns * (kThreads / TPR)) * a.B * a.H;
     norm_gate_rows<T, CH, TPR, GATE><<<grid, kThreads, 0, st>>>(
         static_cast<const T*>(a.y), static_cast<const T*>(a.gate), static_cast<T*>(a.o), a.H, a.N,
         a.dv, a.norm == RET_NORM_LAYER, a.eps, a.token_major != 0, a.ldg, a.ldo);
@@ -187,7 +175,7 @@ template <typename T, bool GATE> cudaError_t forward_t(const NormGateArgs& a, cu
 template <typename T, bool GATE> cudaError_t backward_t(const NormGateArgs& a, cudaStream_t st) {
   return by_width(a.dv * (int)sizeof(T) / 16, [&](auto ch, auto tpr) {
     constexpr int CH = decltype(ch)::value, TPR = decltype(tpr)::value;
-    const dim3 grid(cdiv(a.N, kThreads / TPR), a.B * a.H);
+    const unsigned grid = (unsigned)cdiv(a.N, kTurns * (kThreads / TPR)) * a.B * a.H;
     norm_gate_rows_backward<T, CH, TPR, GATE><<<grid, kThreads, 0, st>>>(
         static_cast<const T*>(a.y), static_cast<const T*>(a.gate), static_cast<const T*>(a.d_o),
         static_cast<T*>(a.grad_y), static_cast<T*>(a.grad_gate), a.H, a.N, a.dv,

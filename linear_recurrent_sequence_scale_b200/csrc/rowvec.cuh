@@ -18,24 +18,175 @@ __device__ __forceinline__ void load_pack(const T* p, float (&x)[V]) {
   for (int i = 0; i < V; ++i) x[i] = Elem<T>::ld(&u.e[i]);
 }
 
-// One rounding (to nearest even) of the float32 value to the storage type.
+// One rounding (to nearest even) of the float32 value to the storage type;
+// two bf16 in one conversion.
 template <typename T, int V>
 __device__ __forceinline__ void store_pack(T* p, const float (&x)[V]) {
   Pack<T, V> u;
+  if constexpr (sizeof(T) == 2 && V % 2 == 0) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) Elem<T>::st(&u.e[i], x[i]);
+    for (int i = 0; i < V; i += 2)
+      *reinterpret_cast<__nv_bfloat162*>(&u.e[i]) = __floats2bfloat162_rn(x[i], x[i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) Elem<T>::st(&u.e[i], x[i]);
+  }
   *reinterpret_cast<Pack<T, V>*>(p) = u;
 }
 
-// sigmoid(x); e^-x overflowing to inf gives 0.
-__device__ __forceinline__ float sigmoidf(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+template <typename T> struct Type { using type = T; };
+template <int I> struct Int { static constexpr int value = I; };
 
-// swish(x) = x sigmoid(x) and its derivative sigmoid(x) (1 + x (1 - sigmoid(x))).
-__device__ __forceinline__ void swish_grad(float x, float* swish, float* slope) {
-  const float s = sigmoidf(x);
-  *swish = x * s;
-  *slope = s * fmaf(x, 1.0f - s, 1.0f);
+// n values computed together; two go through the paired float32 instructions.
+// At 6.5 TB/s an SM has about 31 instruction slots per lane for an element of
+// which 6 bytes move: the kernels below stay under that only with pairs and
+// with the plain hardware exponential and reciprocal.
+template <int n> struct Vec {
+  float v[n];
+};
+template <int n> __device__ __forceinline__ Vec<n> all(float x) {
+  Vec<n> r;
+#pragma unroll
+  for (int i = 0; i < n; ++i) r.v[i] = x;
+  return r;
 }
+__device__ __forceinline__ Vec<1> fma(Vec<1> a, Vec<1> b, Vec<1> c) {
+  return {{fmaf(a.v[0], b.v[0], c.v[0])}};
+}
+__device__ __forceinline__ Vec<2> fma(Vec<2> a, Vec<2> b, Vec<2> c) {
+  Vec<2> r;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.v[0]), "=f"(r.v[1])
+      : "f"(a.v[0]), "f"(a.v[1]), "f"(b.v[0]), "f"(b.v[1]), "f"(c.v[0]), "f"(c.v[1]));
+  return r;
+}
+__device__ __forceinline__ Vec<1> add(Vec<1> a, Vec<1> b) { return {{a.v[0] + b.v[0]}}; }
+__device__ __forceinline__ Vec<2> add(Vec<2> a, Vec<2> b) {
+  Vec<2> r;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.v[0]), "=f"(r.v[1])
+      : "f"(a.v[0]), "f"(a.v[1]), "f"(b.v[0]), "f"(b.v[1]));
+  return r;
+}
+__device__ __forceinline__ Vec<1> mul(Vec<1> a, Vec<1> b) { return {{a.v[0] * b.v[0]}}; }
+__device__ __forceinline__ Vec<2> mul(Vec<2> a, Vec<2> b) {
+  Vec<2> r;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.v[0]), "=f"(r.v[1])
+      : "f"(a.v[0]), "f"(a.v[1]), "f"(b.v[0]), "f"(b.v[1]));
+  return r;
+}
+
+// 2^x and 1/x by the hardware's approximations (2 and 1 units in the last
+// place); 1/x of an infinity is 0.
+template <int n> __device__ __forceinline__ Vec<n> exp2v(Vec<n> x) {
+#pragma unroll
+  for (int i = 0; i < n; ++i) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x.v[i]) : "f"(x.v[i]));
+  return x;
+}
+template <int n> __device__ __forceinline__ Vec<n> rcpv(Vec<n> x) {
+#pragma unroll
+  for (int i = 0; i < n; ++i) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(x.v[i]) : "f"(x.v[i]));
+  return x;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// sigmoid(g) = 1 / (1 + e^-g), an overflow of e^-g giving 0, and swish(g).
+template <int n> __device__ __forceinline__ Vec<n> sigmoid(Vec<n> g) {
+  return rcpv(add(exp2v(mul(g, all<n>(-kLog2e))), all<n>(1.0f)));
+}
+template <int n> __device__ __forceinline__ Vec<n> swish(Vec<n> g) { return mul(g, sigmoid(g)); }
+
+// swish(g) and its derivative sigmoid(g) + swish(g) (1 - sigmoid(g)).
+template <int n>
+__device__ __forceinline__ void swish_grad(Vec<n> g, Vec<n>* sw, Vec<n>* slope) {
+  const Vec<n> s = sigmoid(g);
+  *sw = mul(g, s);
+  *slope = fma(*sw, fma(s, all<n>(-1.0f), all<n>(1.0f)), s);
+}
+
+// E values of a row in one thread's registers, handled in pairs.
+template <int E> __device__ __forceinline__ Vec<2> pair(const float (&v)[E], int i) {
+  return {{v[2 * i], v[2 * i + 1]}};
+}
+template <int E> __device__ __forceinline__ void set_pair(float (&v)[E], int i, Vec<2> x) {
+  v[2 * i] = x.v[0], v[2 * i + 1] = x.v[1];
+}
+__device__ __forceinline__ float total(Vec<2> x) { return x.v[0] + x.v[1]; }
+
+// One thread's part of a row of d = nv V elements: CH accesses of V elements,
+// TPR threads apart.  Elements past d are zeros.
+template <typename T, int V, int CH, int TPR> struct RowPart {
+  static constexpr int E = CH * V, P = E / 2;
+  static_assert(E % 2 == 0, "handled in pairs");
+  float v[E];
+  // `nv` is 0 for a thread whose row does not exist
+  __device__ __forceinline__ void load(const T* p, int lane, int nv) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i = c * TPR + lane;
+      float x[V];
+      if (i < nv) {
+        load_pack<T, V>(p + (long long)i * V, x);
+      } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k) x[k] = 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[c * V + k] = x[k];
+    }
+  }
+  template <typename S>  // stores to another element type share the layout
+  __device__ __forceinline__ void store(S* p, int lane, int nv) const {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i = c * TPR + lane;
+      float x[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) x[k] = v[c * V + k];
+      if (i < nv) store_pack<S, V>(p + (long long)i * V, x);
+    }
+  }
+  // Zeros past d again.
+  __device__ __forceinline__ void clear_rest(int lane, int nv) {
+    if (nv == CH * TPR) return;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      if (c * TPR + lane >= nv) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[c * V + k] = 0.0f;
+      }
+  }
+  // v <- (v - [mean]) r, r = 1 / sqrt(mean square + eps); returns r.  sum(x)
+  // adds x over the row's threads.  A row that does not exist gets r = 0.
+  template <typename Sum>
+  __device__ __forceinline__ float normalise(int lane, int nv, bool layer, float eps, float inv_d,
+                                             Sum sum) {
+    if (layer) {
+      Vec<2> s = all<2>(0.0f);
+#pragma unroll
+      for (int i = 0; i < P; ++i) s = add(s, pair(v, i));
+      const Vec<2> less = all<2>(-sum(total(s), 0) * inv_d);
+#pragma unroll
+      for (int i = 0; i < P; ++i) set_pair(v, i, add(pair(v, i), less));
+      clear_rest(lane, nv);
+    }
+    Vec<2> q = all<2>(0.0f);
+#pragma unroll
+    for (int i = 0; i < P; ++i) q = fma(pair(v, i), pair(v, i), q);
+    const float square = sum(total(q), 1);
+    const float r = nv > 0 ? rsqrtf(fmaf(square, inv_d, eps)) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < P; ++i) set_pair(v, i, mul(pair(v, i), all<2>(r)));
+    return r;
+  }
+};
 
 inline bool aligned_to(const void* p, size_t bytes) {
   return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;

@@ -25,69 +25,6 @@
 namespace ret {
 namespace scan {
 
-template <typename T> struct Type { using type = T; };
-template <int I> struct Int { static constexpr int value = I; };
-
-// The n = 1 or 2 channels that a lane computes together; two go through the
-// paired float32 instructions, which hold the kernels' issue rate under what
-// HBM asks for (one element takes about 12 instruction slots forwards; at
-// 6.5 TB/s there are 31).
-template <int n> struct Vec {
-  float v[n];
-};
-template <int n> __device__ __forceinline__ Vec<n> all(float x) {
-  Vec<n> r;
-#pragma unroll
-  for (int i = 0; i < n; ++i) r.v[i] = x;
-  return r;
-}
-__device__ __forceinline__ Vec<1> fma(Vec<1> a, Vec<1> b, Vec<1> c) {
-  return {{fmaf(a.v[0], b.v[0], c.v[0])}};
-}
-__device__ __forceinline__ Vec<2> fma(Vec<2> a, Vec<2> b, Vec<2> c) {
-  Vec<2> r;
-  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(r.v[0]), "=f"(r.v[1])
-      : "f"(a.v[0]), "f"(a.v[1]), "f"(b.v[0]), "f"(b.v[1]), "f"(c.v[0]), "f"(c.v[1]));
-  return r;
-}
-__device__ __forceinline__ Vec<1> add(Vec<1> a, Vec<1> b) { return {{a.v[0] + b.v[0]}}; }
-__device__ __forceinline__ Vec<2> add(Vec<2> a, Vec<2> b) {
-  Vec<2> r;
-  asm("{\n\t.reg .b64 a, b, d;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(r.v[0]), "=f"(r.v[1])
-      : "f"(a.v[0]), "f"(a.v[1]), "f"(b.v[0]), "f"(b.v[1]));
-  return r;
-}
-__device__ __forceinline__ Vec<1> mul(Vec<1> a, Vec<1> b) { return {{a.v[0] * b.v[0]}}; }
-__device__ __forceinline__ Vec<2> mul(Vec<2> a, Vec<2> b) {
-  Vec<2> r;
-  asm("{\n\t.reg .b64 a, b, d;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(r.v[0]), "=f"(r.v[1])
-      : "f"(a.v[0]), "f"(a.v[1]), "f"(b.v[0]), "f"(b.v[1]));
-  return r;
-}
-
-// 2^x and 1/x by the hardware's approximations (2 and 1 units in the last
-// place); 1/x of an infinity is 0.
-template <int n> __device__ __forceinline__ Vec<n> exp2v(Vec<n> x) {
-#pragma unroll
-  for (int i = 0; i < n; ++i) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x.v[i]) : "f"(x.v[i]));
-  return x;
-}
-template <int n> __device__ __forceinline__ Vec<n> rcpv(Vec<n> x) {
-#pragma unroll
-  for (int i = 0; i < n; ++i) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(x.v[i]) : "f"(x.v[i]));
-  return x;
-}
-constexpr float kLog2e = 1.4426950408889634f;
-
 // q = a - 1.  LOGIT: -1 / (1 + e^f), of full relative precision for every f
 // (an overflow of e^f gives 0).  LOG: e^f - 1, by its Taylor series where the
 // difference would cancel (|f| < 1/4: six terms leave 5e-8 of the value).
@@ -120,12 +57,6 @@ __device__ __forceinline__ Vec<n> advance(Vec<n> z, Vec<n> q, Vec<n> x) {
   const Vec<n> kept = fma(q, z, z);
   return FORM == RET_SCAN_LOGIT ? fma(q, x, kept) : add(kept, x);
 }
-
-// swish(g) and, times dy, what d swish(g) takes and what passes on to h.
-template <int n> __device__ __forceinline__ Vec<n> sigmoid(Vec<n> g) {
-  return rcpv(add(exp2v(mul(g, all<n>(-kLog2e))), all<n>(1.0f)));
-}
-template <int n> __device__ __forceinline__ Vec<n> swish(Vec<n> g) { return mul(g, sigmoid(g)); }
 
 constexpr int kThreads = 128;  // of the single-token kernel
 
@@ -793,10 +724,9 @@ scan_items_backward(const ScanArgs a, const Plan p,
         Q = chain(Q, q[j]);
         dh[j] = get<T>(f + kDy + j * kPiece);
         if constexpr (GATE) {
-          const V g = get<T>(f + kGate + j * kPiece), sig = sigmoid(g), sw = mul(g, sig);
-          // swish'(g) = sig + sw (1 - sig), with the sign of z
-          const V rest = fma(sig, all<n>(-1.0f), all<n>(1.0f));
-          slope[j] = turn<FORM>(mul(dh[j], fma(sw, rest, sig)));
+          V sw, sl;
+          swish_grad(get<T>(f + kGate + j * kPiece), &sw, &sl);
+          slope[j] = turn<FORM>(mul(dh[j], sl));  // with the sign of z
           dh[j] = mul(dh[j], sw);
         }
       }
@@ -889,8 +819,8 @@ __global__ void __launch_bounds__(kThreads) scan_token(const ScanArgs a) {
   load_pack<float, V>(a.state_in + b * a.D + d, z.v);
   load_pack<T, V>(at<T>(a.f, b, 0, d), f.v);
   load_pack<T, V>(at<T>(a.x, b, 0, d), x.v);
-  float g[V];
-  if constexpr (GATE) load_pack<T, V>(at<T>(a.gate, b, 0, d), g);
+  Vec<V> g;
+  if constexpr (GATE) load_pack<T, V>(at<T>(a.gate, b, 0, d), g.v);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const Vec<1> q = less_one<FORM>(Vec<1>{{f.v[v]}});
@@ -899,7 +829,7 @@ __global__ void __launch_bounds__(kThreads) scan_token(const ScanArgs a) {
   store_pack<float, V>(a.state_out + b * a.D + d, z.v);
   if constexpr (GATE) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) z.v[v] *= g[v] * sigmoidf(g[v]);
+    for (int v = 0; v < V; ++v) z.v[v] *= swish(Vec<1>{{g.v[v]}}).v[0];
   }
   store_pack<T, V>(at<T>(a.y, b, 0, d), z.v);
 }
