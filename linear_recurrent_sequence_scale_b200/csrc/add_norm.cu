@@ -23,6 +23,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "rowvec.cuh"
+#include "sm100.cuh"
 
 namespace ret {
 namespace an {
@@ -38,7 +39,7 @@ template <int TPR> __device__ __forceinline__ void row_sum2(float& a, float& b, 
   if constexpr (TPR > 32) {
     constexpr int W = TPR / 32;
     if (threadIdx.x % 32 == 0) slot[threadIdx.x / 32] = make_float2(a, b);
-    __syncthreads();
+    asm volatile("bar.sync 1, %0;" ::"n"(TPR) : "memory");
     a = 0.0f, b = 0.0f;
 #pragma unroll
     for (int w = 0; w < W; ++w) a += slot[w].x, b += slot[w].y;
@@ -148,8 +149,85 @@ add_norm_rows(AddNormArgs a) {
   u.store(static_cast<T*>(a.y) + at, lane, take);
 }
 
-// Persistent over rows: each block sums its rows' weight gradients in
-// registers and leaves one partial row per weight in the workspace.
+// The backward of one row, given ways to load its four tensors (each is called
+// once, x and d_res_out late, when few registers are live), and adding to the
+// weight gradients' partial sums.  read(): every load has been made.
+template <typename G, typename LoadH, typename LoadD, typename LoadS, typename LoadX,
+          typename Read>
+__device__ __forceinline__ void row_backward(const AddNormArgs& a, int lane, int take,
+                                             long long at, bool need_w, bool need_post,
+                                             Row<G>& acc_w, Row<G>& acc_post, float2* slots,
+                                             LoadH load_h, LoadD load_d, LoadS load_s,
+                                             LoadX load_x, Read read) {
+  using T = typename G::type;
+  using R = Row<G>;
+  const float inv_d = 1.0f / a.d;
+  const bool post = a.post_norm != RET_NORM_NONE;
+  R h, d;
+  load_h(h);
+  load_d(d);
+  const float r = h.norm(lane, take, a.norm == RET_NORM_LAYER, a.eps, inv_d, slots);
+  if (need_w) acc_w.add_product(d, h);
+  if (a.w) d.scale(a.w, lane, take);
+  d.norm_backward(h, r, lane, take, a.norm == RET_NORM_LAYER, inv_d, slots + 64);
+  if (a.d_res_out) {
+    R s;
+    load_s(s);
+#pragma unroll
+    for (int i = 0; i < R::P; ++i) set_pair(d.v, i, add(pair(d.v, i), pair(s.v, i)));
+  }
+  R x;
+  if (post || need_post) load_x(x);
+  read();
+  if (a.grad_residual) {
+    R s = d;
+    s.times(a.alpha);
+    s.store(static_cast<T*>(a.grad_residual) + at, lane, take);
+  }
+  d.times(a.beta);
+  float rx = 1.0f;
+  if (post) rx = x.norm(lane, take, a.post_norm == RET_NORM_LAYER, a.eps, inv_d, slots + 96);
+  if (need_post) acc_post.add_product(d, x);
+  if (a.grad_x) {
+    if (a.w_post) d.scale(a.w_post, lane, take);
+    if (post)
+      d.norm_backward(x, rx, lane, take, a.post_norm == RET_NORM_LAYER, inv_d, slots + 160);
+    d.store(static_cast<T*>(a.grad_x) + at, lane, take);
+  }
+}
+
+// A block's sums of the weight gradients, one partial row of the workspace for
+// each of the rows that it works on at a time.
+template <typename G>
+__device__ __forceinline__ void put_partials(const AddNormArgs& a, int lane, int nv, long long part,
+                                             const Row<G>& acc_w, const Row<G>& acc_post,
+                                             float* part_w, float* part_post) {
+  constexpr int Q = G::kV < 4 ? G::kV : 4;
+#pragma unroll
+  for (int c = 0; c < G::kCH; ++c) {
+    const int i = c * G::kTPR + lane;
+    if (i >= nv) continue;
+#pragma unroll
+    for (int k = 0; k < G::kV; k += Q) {
+      float f[Q];
+      const long long to = part * a.d + (long long)i * G::kV + k;
+      if (part_w) {
+#pragma unroll
+        for (int j = 0; j < Q; ++j) f[j] = acc_w.v[c * G::kV + k + j];
+        store_pack<float, Q>(part_w + to, f);
+      }
+      if (part_post) {
+#pragma unroll
+        for (int j = 0; j < Q; ++j) f[j] = acc_post.v[c * G::kV + k + j];
+        store_pack<float, Q>(part_post + to, f);
+      }
+    }
+  }
+}
+
+// Persistent over rows, loads straight into registers: rows that do not split
+// into 16-byte pieces, short ones (several per block), and those too long for
+// the ring below.
 template <typename G>
 __global__ void __launch_bounds__(G::kThreads)
 add_norm_rows_backward(AddNormArgs a, float* part_w, float* part_post) {
@@ -157,8 +235,6 @@ add_norm_rows_backward(AddNormArgs a, float* part_w, float* part_post) {
   using R = Row<G>;
   __shared__ float2 slots[6 * 32];
   const int lane = threadIdx.x % G::kTPR, nv = a.d / G::kV;
-  const float inv_d = 1.0f / a.d;
-  const bool need_x = a.post_norm != RET_NORM_NONE || part_post;
   R acc_w, acc_post;
 #pragma unroll
   for (int i = 0; i < R::E; ++i) acc_w.v[i] = acc_post.v[i] = 0.0f;
@@ -167,48 +243,96 @@ add_norm_rows_backward(AddNormArgs a, float* part_w, float* part_post) {
     const long long n = g * G::kRows + threadIdx.x / G::kTPR;
     const int take = n < a.rows ? nv : 0;
     const long long at = min(n, a.rows - 1) * a.d;
-    R h, d, s, x;
-    h.load(static_cast<const T*>(a.res_out) + at, lane, take);
-    d.load(static_cast<const T*>(a.d_y) + at, lane, take);
-    if (a.d_res_out) s.load(static_cast<const T*>(a.d_res_out) + at, lane, take);
-    if (need_x) x.load(static_cast<const T*>(a.x) + at, lane, take);
-    const float r = h.norm(lane, take, a.norm == RET_NORM_LAYER, a.eps, inv_d, slots);
-    if (part_w) acc_w.add_product(d, h);
-    if (a.w) d.scale(a.w, lane, take);
-    d.norm_backward(h, r, lane, take, a.norm == RET_NORM_LAYER, inv_d, slots + 64);
-    if (a.d_res_out) {
-#pragma unroll
-      for (int i = 0; i < R::P; ++i) set_pair(d.v, i, add(pair(d.v, i), pair(s.v, i)));
-    }
-    if (a.grad_residual) {
-      s = d;
-      s.times(a.alpha);
-      s.store(static_cast<T*>(a.grad_residual) + at, lane, take);
-    }
-    d.times(a.beta);
-    float rx = 1.0f;
-    if (a.post_norm != RET_NORM_NONE)
-      rx = x.norm(lane, take, a.post_norm == RET_NORM_LAYER, a.eps, inv_d, slots + 96);
-    if (part_post) acc_post.add_product(d, x);
-    if (a.grad_x) {
-      if (a.w_post) d.scale(a.w_post, lane, take);
-      if (a.post_norm != RET_NORM_NONE)
-        d.norm_backward(x, rx, lane, take, a.post_norm == RET_NORM_LAYER, inv_d, slots + 160);
-      d.store(static_cast<T*>(a.grad_x) + at, lane, take);
-    }
+    const auto from = [&](const void* p) {
+      return [=](R& row) { row.load(static_cast<const T*>(p) + at, lane, take); };
+    };
+    // everything is asked for at once: nothing else hides the loads' latency
+    R s, x;
+    if (a.d_res_out) from(a.d_res_out)(s);
+    if (a.post_norm != RET_NORM_NONE || part_post) from(a.x)(x);
+    row_backward<G>(
+        a, lane, take, at, part_w != nullptr, part_post != nullptr, acc_w, acc_post, slots,
+        from(a.res_out), from(a.d_y), [&](R& row) { row = s; }, [&](R& row) { row = x; }, [] {});
   }
-  // one partial row per row group of the block
-  const long long part = ((long long)blockIdx.x * G::kRows + threadIdx.x / G::kTPR) * a.d;
-#pragma unroll
-  for (int c = 0; c < G::kCH; ++c) {
-    const int i = c * G::kTPR + lane;
-    if (i >= nv) continue;
-#pragma unroll
-    for (int k = 0; k < G::kV; ++k) {
-      if (part_w) part_w[part + (long long)i * G::kV + k] = acc_w.v[c * G::kV + k];
-      if (part_post) part_post[part + (long long)i * G::kV + k] = acc_post.v[c * G::kV + k];
+  put_partials<G>(a, lane, nv, (long long)blockIdx.x * G::kRows + threadIdx.x / G::kTPR, acc_w,
+                  acc_post, part_w, part_post);
+}
+
+// The same with the rows coming through a ring in shared memory: one more
+// warp copies whole rows (each tensor's is one contiguous piece) a few rows
+// ahead, so HBM stays busy while the block waits for its row's sums.  The
+// registers hold two rows at a time instead of four.  65536 x 4096 in bf16,
+// both norms and both weights: 1027 us with the loads in registers, ANB_US
+// through the ring.
+constexpr int kSiteRing = 811;
+constexpr int kMaxStages = 4;
+template <int THREADS> constexpr int kRingBlocks = THREADS <= 128 ? 4 : THREADS <= 256 ? 2 : 1;
+
+template <typename G>
+__global__ void __launch_bounds__(G::kTPR + 32, kRingBlocks<G::kTPR>)
+add_norm_ring_backward(AddNormArgs a, float* part_w, float* part_post, int stages) {
+  using T = typename G::type;
+  using R = Row<G>;
+  extern __shared__ __align__(128) char ring[];
+  __shared__ float2 slots[6 * 32];
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages];
+  const bool need_x = a.post_norm != RET_NORM_NONE || part_post;
+  const uint32_t row = a.d * (uint32_t)sizeof(T);
+  const uint32_t stage = row * (2 + (a.d_res_out ? 1 : 0) + (need_x ? 1 : 0));
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      sm100::mbar_init(&full[s], 1);
+      sm100::mbar_init(&empty[s], G::kTPR / 32);
     }
+    sm100::fence_mbar_init();
   }
+  __syncthreads();
+  const int lane = threadIdx.x, nv = a.d / G::kV;
+  if (threadIdx.x >= G::kTPR) {
+    if (threadIdx.x > G::kTPR) return;
+    int s = 0, phase = 0;
+    bool first = true;
+    for (long long n = blockIdx.x; n < a.rows; n += gridDim.x) {
+      if (!first && !sm100::mbar_wait(&empty[s], phase ^ 1, kSiteRing)) {
+        for (int i = 0; i < stages; ++i)  // the copies under way end before the block does
+          sm100::mbar_drain(&full[i], i < s ? phase : phase ^ 1);
+        return;
+      }
+      const auto load = [&](const void* p, uint32_t place) {
+        sm100::bulk_load(ring + s * stage + place, static_cast<const T*>(p) + n * a.d, row,
+                         &full[s]);
+      };
+      sm100::mbar_arrive_expect_tx(&full[s], stage);
+      load(a.res_out, 0);
+      load(a.d_y, row);
+      if (a.d_res_out) load(a.d_res_out, 2 * row);
+      if (need_x) load(a.x, stage - row);
+      if (++s == stages) s = 0, phase ^= 1, first = false;
+    }
+    return;
+  }
+  R acc_w, acc_post;
+#pragma unroll
+  for (int i = 0; i < R::E; ++i) acc_w.v[i] = acc_post.v[i] = 0.0f;
+  int s = 0, phase = 0;
+  for (long long n = blockIdx.x; n < a.rows; n += gridDim.x) {
+    sm100::mbar_wait(&full[s], phase, kSiteRing + 1);
+    const T* here = reinterpret_cast<const T*>(ring + s * stage);
+    const auto from = [&](uint32_t place) {
+      return [=](R& part) {
+        part.load(reinterpret_cast<const T*>(reinterpret_cast<const char*>(here) + place), lane,
+                  nv);
+      };
+    };
+    row_backward<G>(
+        a, lane, nv, n * a.d, part_w != nullptr, part_post != nullptr, acc_w, acc_post, slots,
+        from(0), from(row), from(2 * row), from(stage - row), [&] {
+          __syncwarp();
+          if (lane % 32 == 0) sm100::mbar_arrive(&empty[s]);
+        });
+    if (++s == stages) s = 0, phase ^= 1;
+  }
+  put_partials<G>(a, lane, nv, blockIdx.x, acc_w, acc_post, part_w, part_post);
 }
 
 // grad[c] = sum of the partial rows, in a fixed order: 8 warps take every
@@ -288,17 +412,50 @@ cudaError_t launch_add_norm(const AddNormArgs& a, cudaStream_t st) {
   });
 }
 
+namespace an {
+
+// The ring's depth for rows of this size, 0 where it does not serve: fewer
+// than two stages fit, or rows short enough for a warp.
+template <typename G> int ring_stages(const AddNormArgs& a) {
+  if (G::kTPR <= 32 || G::kTPR > 512 || G::kV == 1) return 0;
+  const int tensors = 2 + (a.d_res_out ? 1 : 0) +
+                      (a.post_norm != RET_NORM_NONE || a.grad_w_post ? 1 : 0);
+  const int stage = tensors * a.d * (int)sizeof(typename G::type);
+  const int stages = (220 * 1024 / kRingBlocks<G::kTPR>) / stage;
+  return stages < 2 ? 0 : stages < kMaxStages ? stages : kMaxStages;
+}
+
+}  // namespace an
+
+int add_norm_device_error() { return read_clear_device_error(); }
+
 cudaError_t launch_add_norm_backward(const AddNormArgs& a, float* ws, cudaStream_t st) {
   return an::by_geometry(a, [&](auto geo) {
     using G = decltype(geo);
     const long long groups = (a.rows + G::kRows - 1) / G::kRows;
-    const int grid = static_cast<int>(groups < an::kMaxBlocks ? groups : an::kMaxBlocks);
+    int most = an::kMaxBlocks;
+    const int stages = an::ring_stages<G>(a);
+    if (stages) most = most / 4 * an::kRingBlocks<G::kTPR>;
+    const int grid = static_cast<int>(groups < most ? groups : most);
     const int parts = grid * G::kRows;
     float* part_w = a.grad_w ? ws : nullptr;
     float* part_post =
         a.grad_w_post ? ws + (a.grad_w ? (size_t)parts * a.d : (size_t)0) : nullptr;
-    an::add_norm_rows_backward<G><<<grid, G::kThreads, 0, st>>>(a, part_w, part_post);
-    cudaError_t e = cudaPeekAtLastError();
+    cudaError_t e = cudaSuccess;
+    if constexpr (G::kTPR > 32 && G::kTPR <= 512 && G::kV > 1) {
+      if (stages) {
+        const int tensors = 2 + (a.d_res_out ? 1 : 0) +
+                            (a.post_norm != RET_NORM_NONE || part_post ? 1 : 0);
+        const int smem = stages * tensors * a.d * (int)sizeof(typename G::type);
+        e = cudaFuncSetAttribute(an::add_norm_ring_backward<G>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        an::add_norm_ring_backward<G>
+            <<<grid, G::kTPR + 32, smem, st>>>(a, part_w, part_post, stages);
+      }
+    }
+    if (!stages) an::add_norm_rows_backward<G><<<grid, G::kThreads, 0, st>>>(a, part_w, part_post);
+    e = cudaPeekAtLastError();
     if (e != cudaSuccess || !(part_w || part_post)) return e;
     an::sum_partials<<<dim3(cdiv(a.d, 32), 2), 32 * an::kReduceWarps, 0, st>>>(
         part_w, part_post, a.grad_w, a.grad_w_post, parts, a.d);

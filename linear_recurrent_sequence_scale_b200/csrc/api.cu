@@ -76,8 +76,9 @@ int ret_device_error(void) {
   const int b = ret::tc_out_device_error();
   const int c = ret::selftest_device_error();
   const int d = ret::scan_device_error();
-  if (a < 0 || b < 0 || c < 0 || d < 0) return -1;
-  return a ? a : (b ? b : (c ? c : d));
+  const int e = ret::add_norm_device_error();
+  if (a < 0 || b < 0 || c < 0 || d < 0 || e < 0) return -1;
+  return a ? a : (b ? b : (c ? c : (d ? d : e)));
 }
 
 int ret_selftest_bounded_wait(int limit_ms, void* stream) {

@@ -97,6 +97,7 @@ struct AddNormArgs {
   float alpha, beta, eps;
 };
 size_t add_norm_backward_workspace_bytes(long long rows, int d);
+int add_norm_device_error();
 cudaError_t launch_add_norm(const AddNormArgs& a, cudaStream_t st);
 cudaError_t launch_add_norm_backward(const AddNormArgs& a, float* ws, cudaStream_t st);
 

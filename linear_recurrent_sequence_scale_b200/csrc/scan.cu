@@ -471,12 +471,8 @@ __device__ __forceinline__ void mover(Desk<STAGES, n>& desk, char* ring, const P
   sm100::bulk_wait0();
   if (!ok) {  // some wait gave up: the loads under way still end before the block does
 #pragma unroll
-    for (int s = 0; s < STAGES; ++s) {
-      const uint64_t t0 = sm100::globaltimer();
-      while (loads[s] > 0 && !sm100::mbar_try_wait(&desk.loaded[s], (loads[s] - 1) % 2) &&
-             sm100::globaltimer() - t0 < sm100::kWaitLimitNs) {
-      }
-    }
+    for (int s = 0; s < STAGES; ++s)
+      if (loads[s] > 0) sm100::mbar_drain(&desk.loaded[s], (loads[s] - 1) % 2);
   }
 }
 
