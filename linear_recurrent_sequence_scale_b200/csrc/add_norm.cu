@@ -149,53 +149,6 @@ add_norm_rows(AddNormArgs a) {
   u.store(static_cast<T*>(a.y) + at, lane, take);
 }
 
-// The backward of one row, given ways to load its four tensors (each is called
-// once, x and d_res_out late, when few registers are live), and adding to the
-// weight gradients' partial sums.  read(): every load has been made.
-template <typename G, typename LoadH, typename LoadD, typename LoadS, typename LoadX,
-          typename Read>
-__device__ __forceinline__ void row_backward(const AddNormArgs& a, int lane, int take,
-                                             long long at, bool need_w, bool need_post,
-                                             Row<G>& acc_w, Row<G>& acc_post, float2* slots,
-                                             LoadH load_h, LoadD load_d, LoadS load_s,
-                                             LoadX load_x, Read read) {
-  using T = typename G::type;
-  using R = Row<G>;
-  const float inv_d = 1.0f / a.d;
-  const bool post = a.post_norm != RET_NORM_NONE;
-  R h, d;
-  load_h(h);
-  load_d(d);
-  const float r = h.norm(lane, take, a.norm == RET_NORM_LAYER, a.eps, inv_d, slots);
-  if (need_w) acc_w.add_product(d, h);
-  if (a.w) d.scale(a.w, lane, take);
-  d.norm_backward(h, r, lane, take, a.norm == RET_NORM_LAYER, inv_d, slots + 64);
-  if (a.d_res_out) {
-    R s;
-    load_s(s);
-#pragma unroll
-    for (int i = 0; i < R::P; ++i) set_pair(d.v, i, add(pair(d.v, i), pair(s.v, i)));
-  }
-  R x;
-  if (post || need_post) load_x(x);
-  read();
-  if (a.grad_residual) {
-    R s = d;
-    s.times(a.alpha);
-    s.store(static_cast<T*>(a.grad_residual) + at, lane, take);
-  }
-  d.times(a.beta);
-  float rx = 1.0f;
-  if (post) rx = x.norm(lane, take, a.post_norm == RET_NORM_LAYER, a.eps, inv_d, slots + 96);
-  if (need_post) acc_post.add_product(d, x);
-  if (a.grad_x) {
-    if (a.w_post) d.scale(a.w_post, lane, take);
-    if (post)
-      d.norm_backward(x, rx, lane, take, a.post_norm == RET_NORM_LAYER, inv_d, slots + 160);
-    d.store(static_cast<T*>(a.grad_x) + at, lane, take);
-  }
-}
-
 // A block's sums of the weight gradients, one partial row of the workspace for
 // each of the rows that it works on at a time.
 template <typename G>
@@ -235,6 +188,8 @@ add_norm_rows_backward(AddNormArgs a, float* part_w, float* part_post) {
   using R = Row<G>;
   __shared__ float2 slots[6 * 32];
   const int lane = threadIdx.x % G::kTPR, nv = a.d / G::kV;
+  const float inv_d = 1.0f / a.d;
+  const bool post = a.post_norm != RET_NORM_NONE;
   R acc_w, acc_post;
 #pragma unroll
   for (int i = 0; i < R::E; ++i) acc_w.v[i] = acc_post.v[i] = 0.0f;
@@ -243,16 +198,34 @@ add_norm_rows_backward(AddNormArgs a, float* part_w, float* part_post) {
     const long long n = g * G::kRows + threadIdx.x / G::kTPR;
     const int take = n < a.rows ? nv : 0;
     const long long at = min(n, a.rows - 1) * a.d;
-    const auto from = [&](const void* p) {
-      return [=](R& row) { row.load(static_cast<const T*>(p) + at, lane, take); };
-    };
-    // everything is asked for at once: nothing else hides the loads' latency
-    R s, x;
-    if (a.d_res_out) from(a.d_res_out)(s);
-    if (a.post_norm != RET_NORM_NONE || part_post) from(a.x)(x);
-    row_backward<G>(
-        a, lane, take, at, part_w != nullptr, part_post != nullptr, acc_w, acc_post, slots,
-        from(a.res_out), from(a.d_y), [&](R& row) { row = s; }, [&](R& row) { row = x; }, [] {});
+    R h, d, s, x;
+    h.load(static_cast<const T*>(a.res_out) + at, lane, take);
+    d.load(static_cast<const T*>(a.d_y) + at, lane, take);
+    if (a.d_res_out) s.load(static_cast<const T*>(a.d_res_out) + at, lane, take);
+    if (post || part_post) x.load(static_cast<const T*>(a.x) + at, lane, take);
+    const float r = h.norm(lane, take, a.norm == RET_NORM_LAYER, a.eps, inv_d, slots);
+    if (part_w) acc_w.add_product(d, h);
+    if (a.w) d.scale(a.w, lane, take);
+    d.norm_backward(h, r, lane, take, a.norm == RET_NORM_LAYER, inv_d, slots + 64);
+    if (a.d_res_out) {
+#pragma unroll
+      for (int i = 0; i < R::P; ++i) set_pair(d.v, i, add(pair(d.v, i), pair(s.v, i)));
+    }
+    if (a.grad_residual) {
+      s = d;
+      s.times(a.alpha);
+      s.store(static_cast<T*>(a.grad_residual) + at, lane, take);
+    }
+    d.times(a.beta);
+    float rx = 1.0f;
+    if (post) rx = x.norm(lane, take, a.post_norm == RET_NORM_LAYER, a.eps, inv_d, slots + 96);
+    if (part_post) acc_post.add_product(d, x);
+    if (a.grad_x) {
+      if (a.w_post) d.scale(a.w_post, lane, take);
+      if (post)
+        d.norm_backward(x, rx, lane, take, a.post_norm == RET_NORM_LAYER, inv_d, slots + 160);
+      d.store(static_cast<T*>(a.grad_x) + at, lane, take);
+    }
   }
   put_partials<G>(a, lane, nv, (long long)blockIdx.x * G::kRows + threadIdx.x / G::kTPR, acc_w,
                   acc_post, part_w, part_post);
@@ -260,31 +233,187 @@ add_norm_rows_backward(AddNormArgs a, float* part_w, float* part_post) {
 
 // The same with the rows coming through a ring in shared memory: one more
 // warp copies whole rows (each tensor's is one contiguous piece) a few rows
-// ahead, so HBM stays busy while the block waits for its row's sums.  The
-// registers hold two rows at a time instead of four.  65536 x 4096 in bf16,
-// both norms and both weights: 1027 us with the loads in registers, ANB_US
-// through the ring.
+// ahead, so HBM stays busy while the block waits for its row's sums.  What
+// remains is instructions (about 30 per element; HBM allows 62), so the sums
+// are few: both norms' moments cross the block in one exchange, each warp
+// taking its own about its own mean and the block joining them (Chan, Golub
+// and LeVeque's pairwise variance), and the weights wait in shared memory.
+// 65536 x 4096 in bf16, both norms and both weights: 1027 us with loads in
+// registers and five exchanges, 903 through the ring, ANB_US with three.
 constexpr int kSiteRing = 811;
 constexpr int kMaxStages = 4;
 template <int THREADS> constexpr int kRingBlocks = THREADS <= 128 ? 4 : THREADS <= 256 ? 2 : 1;
+
+__device__ __forceinline__ Vec<2> warp_sum(Vec<2> x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    x = add(x, Vec<2>{{__shfl_xor_sync(0xffffffffu, x.v[0], o),
+                       __shfl_xor_sync(0xffffffffu, x.v[1], o)}});
+  return x;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// A row's mean (0 for RMS) and 1 / spread.
+struct Moments {
+  float mean, r;
+};
+
+template <typename G> struct Block {
+  static constexpr int W = G::kTPR / 32;
+  static constexpr int kLane = G::kCH * G::kV;  // elements of a thread in a full row
+  static __device__ __forceinline__ void sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(G::kTPR) : "memory");
+  }
+  // Elements of the row that warp w holds.
+  static __device__ __forceinline__ int held(int w, int nv) {
+    int n = 0;
+#pragma unroll
+    for (int c = 0; c < G::kCH; ++c) n += min(max(nv - (c * G::kTPR + w * 32), 0), 32);
+    return n * G::kV;
+  }
+  // One warp's mean (layer) and sum of squares about it.
+  static __device__ __forceinline__ float2 own(const Row<G>& v, bool layer, int lane, int nv) {
+    using R = Row<G>;
+    float mean = 0.0f;
+    if (layer) {
+      Vec<2> s = all<2>(0.0f);
+#pragma unroll
+      for (int i = 0; i < R::P; ++i) s = add(s, pair(v.v, i));
+      const int n = nv == G::kCH * G::kTPR ? 32 * kLane : held(lane / 32, nv);
+      const float sum = warp_sum(total(s));
+      mean = n > 0 ? __fdividef(sum, (float)n) : 0.0f;
+    }
+    Vec<2> q = all<2>(0.0f);
+    if (layer) {
+      R t = v;
+#pragma unroll
+      for (int i = 0; i < R::P; ++i) set_pair(t.v, i, add(pair(t.v, i), all<2>(-mean)));
+      t.clear_rest(lane, nv);
+#pragma unroll
+      for (int i = 0; i < R::P; ++i) q = fma(pair(t.v, i), pair(t.v, i), q);
+    } else {
+#pragma unroll
+      for (int i = 0; i < R::P; ++i) q = fma(pair(v.v, i), pair(v.v, i), q);
+    }
+    return make_float2(mean, total(q));  // the squares still spread over the lanes
+  }
+  // The row's moments from the warps' (.x mean, .y sum of squares about it).
+  template <typename Get>
+  static __device__ __forceinline__ Moments join(Get get, bool layer, float eps, float inv_d,
+                                                 int nv) {
+    float mean = 0.0f, m2 = 0.0f;
+    if (!layer) {
+#pragma unroll
+      for (int w = 0; w < W; ++w) m2 += get(w).y;
+    } else if (nv == G::kCH * G::kTPR) {  // every warp holds as much
+      float apart = 0.0f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) mean += get(w).x;
+      mean *= 1.0f / W;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float2 g = get(w);
+        m2 += g.y;
+        apart = fmaf(g.x - mean, g.x - mean, apart);
+      }
+      m2 = fmaf(apart, 32.0f * kLane, m2);
+    } else {
+      for (int w = 0; w < W; ++w) mean = fmaf(get(w).x, held(w, nv) * inv_d, mean);
+      for (int w = 0; w < W; ++w) {
+        const float2 g = get(w);
+        m2 += fmaf((g.x - mean) * (g.x - mean), (float)held(w, nv), g.y);
+      }
+    }
+    return {mean, rsqrtf(fmaf(m2, inv_d, eps))};
+  }
+  // Both sums over the block.
+  static __device__ __forceinline__ Vec<2> sum(Vec<2> x, float2* slot) {
+    x = warp_sum(x);
+    if (threadIdx.x % 32 == 0) slot[threadIdx.x / 32] = make_float2(x.v[0], x.v[1]);
+    sync();
+    Vec<2> s = all<2>(0.0f);
+#pragma unroll
+    for (int w = 0; w < W; w += 2) {
+      const float4 f = *reinterpret_cast<const float4*>(slot + w);
+      s = add(s, add(Vec<2>{{f.x, f.y}}, Vec<2>{{f.z, f.w}}));
+    }
+    return s;
+  }
+  // v <- (v - mean) r
+  static __device__ __forceinline__ void apply(Row<G>& v, Moments m, bool layer, int lane,
+                                               int nv) {
+#pragma unroll
+    for (int i = 0; i < Row<G>::P; ++i)
+      set_pair(v.v, i, fma(pair(v.v, i), all<2>(m.r), all<2>(-m.mean * m.r)));
+    if (layer) v.clear_rest(lane, nv);
+  }
+  // d <- r (d - [mean(d)] - h mean(d (.) h))
+  static __device__ __forceinline__ void back(Row<G>& d, const Row<G>& h, float r, bool layer,
+                                              float inv_d, float2* slot, int lane, int nv) {
+    using R = Row<G>;
+    Vec<2> p1 = all<2>(0.0f), p2 = p1;
+#pragma unroll
+    for (int i = 0; i < R::P; ++i) {
+      p1 = add(p1, pair(d.v, i));
+      p2 = fma(pair(d.v, i), pair(h.v, i), p2);
+    }
+    const Vec<2> s = sum(Vec<2>{{total(p1), total(p2)}}, slot);
+    const float s1 = layer ? s.v[0] * -inv_d : 0.0f, s2 = s.v[1] * -inv_d;
+#pragma unroll
+    for (int i = 0; i < R::P; ++i)
+      set_pair(d.v, i,
+               mul(all<2>(r), fma(pair(h.v, i), all<2>(s2), add(pair(d.v, i), all<2>(s1)))));
+    if (layer) d.clear_rest(lane, nv);
+  }
+  // v <- v (.) w
+  static __device__ __forceinline__ void scale(Row<G>& v, const float* w, int lane, int nv) {
+#pragma unroll
+    for (int c = 0; c < G::kCH; ++c) {
+      const int i = c * G::kTPR + lane;
+      if (i < nv) {
+#pragma unroll
+        for (int j = 0; j < G::kV; j += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(w + i * G::kV + j);
+          const int k = (c * G::kV + j) / 2;
+          set_pair(v.v, k, mul(pair(v.v, k), Vec<2>{{f.x, f.y}}));
+          set_pair(v.v, k + 1, mul(pair(v.v, k + 1), Vec<2>{{f.z, f.w}}));
+        }
+      }
+    }
+  }
+};
 
 template <typename G>
 __global__ void __launch_bounds__(G::kTPR + 32, kRingBlocks<G::kTPR>)
 add_norm_ring_backward(AddNormArgs a, float* part_w, float* part_post, int stages) {
   using T = typename G::type;
   using R = Row<G>;
+  using B = Block<G>;
   extern __shared__ __align__(128) char ring[];
-  __shared__ float2 slots[6 * 32];
+  __shared__ float4 moments[B::W];
+  __shared__ __align__(16) float2 slots[2][B::W];
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages];
-  const bool need_x = a.post_norm != RET_NORM_NONE || part_post;
+  const bool post = a.post_norm != RET_NORM_NONE, need_x = post || part_post;
+  const bool layer = a.norm == RET_NORM_LAYER, layer_post = a.post_norm == RET_NORM_LAYER;
   const uint32_t row = a.d * (uint32_t)sizeof(T);
   const uint32_t stage = row * (2 + (a.d_res_out ? 1 : 0) + (need_x ? 1 : 0));
+  // behind the ring, the weights
+  float* w = reinterpret_cast<float*>(ring + stages * stage);
+  float* w_post = w + (a.w ? a.d : 0);
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
       sm100::mbar_init(&full[s], 1);
-      sm100::mbar_init(&empty[s], G::kTPR / 32);
+      sm100::mbar_init(&empty[s], B::W);
     }
     sm100::fence_mbar_init();
+  }
+  for (int i = threadIdx.x; i < a.d; i += G::kTPR + 32) {
+    if (a.w) w[i] = a.w[i];
+    if (a.w_post) w_post[i] = a.w_post[i];
   }
   __syncthreads();
   const int lane = threadIdx.x, nv = a.d / G::kV;
@@ -311,25 +440,63 @@ add_norm_ring_backward(AddNormArgs a, float* part_w, float* part_post, int stage
     }
     return;
   }
+  const float inv_d = 1.0f / a.d;
   R acc_w, acc_post;
 #pragma unroll
   for (int i = 0; i < R::E; ++i) acc_w.v[i] = acc_post.v[i] = 0.0f;
   int s = 0, phase = 0;
   for (long long n = blockIdx.x; n < a.rows; n += gridDim.x) {
     sm100::mbar_wait(&full[s], phase, kSiteRing + 1);
-    const T* here = reinterpret_cast<const T*>(ring + s * stage);
-    const auto from = [&](uint32_t place) {
-      return [=](R& part) {
-        part.load(reinterpret_cast<const T*>(reinterpret_cast<const char*>(here) + place), lane,
-                  nv);
-      };
+    const auto load = [&](R& part, uint32_t place) {
+      part.load(reinterpret_cast<const T*>(ring + s * stage + place), lane, nv);
     };
-    row_backward<G>(
-        a, lane, nv, n * a.d, part_w != nullptr, part_post != nullptr, acc_w, acc_post, slots,
-        from(0), from(row), from(2 * row), from(stage - row), [&] {
-          __syncwarp();
-          if (lane % 32 == 0) sm100::mbar_arrive(&empty[s]);
-        });
+    const long long at = n * a.d;
+    R h, d;
+    // both norms' moments
+    float2 mine_x = make_float2(0.0f, 0.0f);
+    if (post) {
+      load(d, stage - row);
+      mine_x = B::own(d, layer_post, lane, nv);
+    }
+    load(h, 0);
+    const float2 mine_h = B::own(h, layer, lane, nv);
+    const Vec<2> m2 = warp_sum(Vec<2>{{mine_h.y, mine_x.y}});
+    if (lane % 32 == 0) moments[lane / 32] = make_float4(mine_h.x, m2.v[0], mine_x.x, m2.v[1]);
+    B::sync();
+    const Moments mh = B::join(
+        [&](int i) { return make_float2(moments[i].x, moments[i].y); }, layer, a.eps, inv_d, nv);
+    Moments mx = {0.0f, 1.0f};
+    if (post)
+      mx = B::join([&](int i) { return make_float2(moments[i].z, moments[i].w); }, layer_post,
+                   a.eps, inv_d, nv);
+    // through the norm before the next block
+    B::apply(h, mh, layer, lane, nv);
+    load(d, row);
+    if (part_w) acc_w.add_product(d, h);
+    if (a.w) B::scale(d, w, lane, nv);
+    B::back(d, h, mh.r, layer, inv_d, slots[0], lane, nv);
+    if (a.d_res_out) {
+      load(h, 2 * row);
+#pragma unroll
+      for (int i = 0; i < R::P; ++i) set_pair(d.v, i, add(pair(d.v, i), pair(h.v, i)));
+    }
+    if (a.grad_residual) {
+      h = d;
+      h.times(a.alpha);
+      h.store(static_cast<T*>(a.grad_residual) + at, lane, nv);
+    }
+    d.times(a.beta);
+    // and through the one after the block
+    if (need_x) load(h, stage - row);
+    __syncwarp();
+    if (lane % 32 == 0) sm100::mbar_arrive(&empty[s]);
+    if (post) B::apply(h, mx, layer_post, lane, nv);
+    if (part_post) acc_post.add_product(d, h);
+    if (a.grad_x) {
+      if (a.w_post) B::scale(d, w_post, lane, nv);
+      if (post) B::back(d, h, mx.r, layer_post, inv_d, slots[1], lane, nv);
+      d.store(static_cast<T*>(a.grad_x) + at, lane, nv);
+    }
     if (++s == stages) s = 0, phase ^= 1;
   }
   put_partials<G>(a, lane, nv, blockIdx.x, acc_w, acc_post, part_w, part_post);
@@ -414,15 +581,20 @@ cudaError_t launch_add_norm(const AddNormArgs& a, cudaStream_t st) {
 
 namespace an {
 
-// The ring's depth for rows of this size, 0 where it does not serve: fewer
-// than two stages fit, or rows short enough for a warp.
-template <typename G> int ring_stages(const AddNormArgs& a) {
+// Shared memory of the ring kernel for rows of this size, and its depth; 0
+// where it does not serve: fewer than two stages fit, or rows short enough for
+// a warp.
+template <typename G> int ring_bytes(const AddNormArgs& a, int* stages) {
+  *stages = 0;
   if (G::kTPR <= 32 || G::kTPR > 512 || G::kV == 1) return 0;
   const int tensors = 2 + (a.d_res_out ? 1 : 0) +
                       (a.post_norm != RET_NORM_NONE || a.grad_w_post ? 1 : 0);
   const int stage = tensors * a.d * (int)sizeof(typename G::type);
-  const int stages = (220 * 1024 / kRingBlocks<G::kTPR>) / stage;
-  return stages < 2 ? 0 : stages < kMaxStages ? stages : kMaxStages;
+  const int weights = a.d * 4 * ((a.w ? 1 : 0) + (a.w_post ? 1 : 0));
+  const int n = (220 * 1024 / kRingBlocks<G::kTPR> - weights) / stage;
+  if (n < 2) return 0;
+  *stages = n < kMaxStages ? n : kMaxStages;
+  return *stages * stage + weights;
 }
 
 }  // namespace an
@@ -434,7 +606,8 @@ cudaError_t launch_add_norm_backward(const AddNormArgs& a, float* ws, cudaStream
     using G = decltype(geo);
     const long long groups = (a.rows + G::kRows - 1) / G::kRows;
     int most = an::kMaxBlocks;
-    const int stages = an::ring_stages<G>(a);
+    int stages = 0;
+    const int smem = an::ring_bytes<G>(a, &stages);
     if (stages) most = most / 4 * an::kRingBlocks<G::kTPR>;
     const int grid = static_cast<int>(groups < most ? groups : most);
     const int parts = grid * G::kRows;
@@ -444,9 +617,6 @@ cudaError_t launch_add_norm_backward(const AddNormArgs& a, float* ws, cudaStream
     cudaError_t e = cudaSuccess;
     if constexpr (G::kTPR > 32 && G::kTPR <= 512 && G::kV > 1) {
       if (stages) {
-        const int tensors = 2 + (a.d_res_out ? 1 : 0) +
-                            (a.post_norm != RET_NORM_NONE || part_post ? 1 : 0);
-        const int smem = stages * tensors * a.d * (int)sizeof(typename G::type);
         e = cudaFuncSetAttribute(an::add_norm_ring_backward<G>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
