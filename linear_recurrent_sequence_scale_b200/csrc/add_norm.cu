@@ -65,7 +65,7 @@ struct Row : RowPart<typename G::type, G::kV, G::kCH, G::kTPR> {
   static constexpr int V = G::kV, CH = G::kCH, TPR = G::kTPR;
   using Base = RowPart<typename G::type, V, CH, TPR>;
   using Base::P;
-  using Base::v;
+  using Base::p;
   // v <- v (.) w
   __device__ __forceinline__ void scale(const float* w, int lane, int nv) {
     constexpr int Q = V < 4 ? V : 4;
@@ -78,7 +78,7 @@ struct Row : RowPart<typename G::type, G::kV, G::kCH, G::kTPR> {
           float f[Q];
           load_pack<float, Q>(w + (long long)i * V + j, f);
 #pragma unroll
-          for (int k = 0; k < Q; ++k) v[c * V + j + k] *= f[k];
+          for (int k = 0; k < Q; ++k) this->put(c * V + j + k, this->get(c * V + j + k) * f[k]);
         }
       }
     }
@@ -96,8 +96,8 @@ struct Row : RowPart<typename G::type, G::kV, G::kCH, G::kTPR> {
     Vec<2> p1 = all<2>(0.0f), p2 = p1;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      p1 = add(p1, pair(v, i));
-      p2 = fma(pair(v, i), pair(h.v, i), p2);
+      p1 = add(p1, p[i]);
+      p2 = fma(p[i], h.p[i], p2);
     }
     float s1 = total(p1), s2 = total(p2);
     row_sum2<TPR>(s1, s2, slot);
@@ -105,18 +105,17 @@ struct Row : RowPart<typename G::type, G::kV, G::kCH, G::kTPR> {
     s2 *= -inv_d;
 #pragma unroll
     for (int i = 0; i < P; ++i)
-      set_pair(v, i,
-               mul(all<2>(r), fma(pair(h.v, i), all<2>(s2), add(pair(v, i), all<2>(s1)))));
+      p[i] = mul(all<2>(r), fma(h.p[i], all<2>(s2), add(p[i], all<2>(s1))));
     if (layer) this->clear_rest(lane, nv);
   }
   // v <- v + a (.) b
   __device__ __forceinline__ void add_product(const Row& a, const Row& b) {
 #pragma unroll
-    for (int i = 0; i < P; ++i) set_pair(v, i, fma(pair(a.v, i), pair(b.v, i), pair(v, i)));
+    for (int i = 0; i < P; ++i) p[i] = fma(a.p[i], b.p[i], p[i]);
   }
   __device__ __forceinline__ void times(float f) {
 #pragma unroll
-    for (int i = 0; i < P; ++i) set_pair(v, i, mul(pair(v, i), all<2>(f)));
+    for (int i = 0; i < P; ++i) p[i] = mul(p[i], all<2>(f));
   }
 };
 
@@ -141,7 +140,7 @@ add_norm_rows(AddNormArgs a) {
   if (a.residual) {
 #pragma unroll
     for (int i = 0; i < R::P; ++i)
-      set_pair(u.v, i, fma(all<2>(a.alpha), pair(s.v, i), pair(u.v, i)));
+      u.p[i] = fma(all<2>(a.alpha), s.p[i], u.p[i]);
   }
   u.store(static_cast<T*>(a.res_out) + at, lane, take);
   u.norm(lane, take, a.norm == RET_NORM_LAYER, a.eps, inv_d, slots + 64);
@@ -166,12 +165,12 @@ __device__ __forceinline__ void put_partials(const AddNormArgs& a, int lane, int
       const long long to = part * a.d + (long long)i * G::kV + k;
       if (part_w) {
 #pragma unroll
-        for (int j = 0; j < Q; ++j) f[j] = acc_w.v[c * G::kV + k + j];
+        for (int j = 0; j < Q; ++j) f[j] = acc_w.get(c * G::kV + k + j);
         store_pack<float, Q>(part_w + to, f);
       }
       if (part_post) {
 #pragma unroll
-        for (int j = 0; j < Q; ++j) f[j] = acc_post.v[c * G::kV + k + j];
+        for (int j = 0; j < Q; ++j) f[j] = acc_post.get(c * G::kV + k + j);
         store_pack<float, Q>(part_post + to, f);
       }
     }
@@ -192,7 +191,7 @@ add_norm_rows_backward(AddNormArgs a, float* part_w, float* part_post) {
   const bool post = a.post_norm != RET_NORM_NONE;
   R acc_w, acc_post;
 #pragma unroll
-  for (int i = 0; i < R::E; ++i) acc_w.v[i] = acc_post.v[i] = 0.0f;
+  for (int i = 0; i < R::P; ++i) acc_w.p[i] = acc_post.p[i] = all<2>(0.0f);
   const long long groups = (a.rows + G::kRows - 1) / G::kRows;
   for (long long g = blockIdx.x; g < groups; g += gridDim.x) {
     const long long n = g * G::kRows + threadIdx.x / G::kTPR;
@@ -209,7 +208,7 @@ add_norm_rows_backward(AddNormArgs a, float* part_w, float* part_post) {
     d.norm_backward(h, r, lane, take, a.norm == RET_NORM_LAYER, inv_d, slots + 64);
     if (a.d_res_out) {
 #pragma unroll
-      for (int i = 0; i < R::P; ++i) set_pair(d.v, i, add(pair(d.v, i), pair(s.v, i)));
+      for (int i = 0; i < R::P; ++i) d.p[i] = add(d.p[i], s.p[i]);
     }
     if (a.grad_residual) {
       s = d;
@@ -247,8 +246,8 @@ template <int THREADS> constexpr int kRingBlocks = THREADS <= 128 ? 4 : THREADS 
 __device__ __forceinline__ Vec<2> warp_sum(Vec<2> x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
-    x = add(x, Vec<2>{{__shfl_xor_sync(0xffffffffu, x.v[0], o),
-                       __shfl_xor_sync(0xffffffffu, x.v[1], o)}});
+    x = add(x, two(__shfl_xor_sync(0xffffffffu, x[0], o),
+                   __shfl_xor_sync(0xffffffffu, x[1], o)));
   return x;
 }
 __device__ __forceinline__ float warp_sum(float x) {
@@ -282,7 +281,7 @@ template <typename G> struct Block {
     if (layer) {
       Vec<2> s = all<2>(0.0f);
 #pragma unroll
-      for (int i = 0; i < R::P; ++i) s = add(s, pair(v.v, i));
+      for (int i = 0; i < R::P; ++i) s = add(s, v.p[i]);
       const int n = nv == G::kCH * G::kTPR ? 32 * kLane : held(lane / 32, nv);
       const float sum = warp_sum(total(s));
       mean = n > 0 ? __fdividef(sum, (float)n) : 0.0f;
@@ -291,13 +290,13 @@ template <typename G> struct Block {
     if (layer) {
       R t = v;
 #pragma unroll
-      for (int i = 0; i < R::P; ++i) set_pair(t.v, i, add(pair(t.v, i), all<2>(-mean)));
+      for (int i = 0; i < R::P; ++i) t.p[i] = add(t.p[i], all<2>(-mean));
       t.clear_rest(lane, nv);
 #pragma unroll
-      for (int i = 0; i < R::P; ++i) q = fma(pair(t.v, i), pair(t.v, i), q);
+      for (int i = 0; i < R::P; ++i) q = fma(t.p[i], t.p[i], q);
     } else {
 #pragma unroll
-      for (int i = 0; i < R::P; ++i) q = fma(pair(v.v, i), pair(v.v, i), q);
+      for (int i = 0; i < R::P; ++i) q = fma(v.p[i], v.p[i], q);
     }
     return make_float2(mean, total(q));  // the squares still spread over the lanes
   }
@@ -333,13 +332,13 @@ template <typename G> struct Block {
   // Both sums over the block.
   static __device__ __forceinline__ Vec<2> sum(Vec<2> x, float2* slot) {
     x = warp_sum(x);
-    if (threadIdx.x % 32 == 0) slot[threadIdx.x / 32] = make_float2(x.v[0], x.v[1]);
+    if (threadIdx.x % 32 == 0) slot[threadIdx.x / 32] = make_float2(x[0], x[1]);
     sync();
     Vec<2> s = all<2>(0.0f);
 #pragma unroll
     for (int w = 0; w < W; w += 2) {
       const float4 f = *reinterpret_cast<const float4*>(slot + w);
-      s = add(s, add(Vec<2>{{f.x, f.y}}, Vec<2>{{f.z, f.w}}));
+      s = add(s, add(two(f.x, f.y), two(f.z, f.w)));
     }
     return s;
   }
@@ -348,7 +347,7 @@ template <typename G> struct Block {
                                                int nv) {
 #pragma unroll
     for (int i = 0; i < Row<G>::P; ++i)
-      set_pair(v.v, i, fma(pair(v.v, i), all<2>(m.r), all<2>(-m.mean * m.r)));
+      v.p[i] = fma(v.p[i], all<2>(m.r), all<2>(-m.mean * m.r));
     if (layer) v.clear_rest(lane, nv);
   }
   // d <- r (d - [mean(d)] - h mean(d (.) h))
@@ -358,15 +357,14 @@ template <typename G> struct Block {
     Vec<2> p1 = all<2>(0.0f), p2 = p1;
 #pragma unroll
     for (int i = 0; i < R::P; ++i) {
-      p1 = add(p1, pair(d.v, i));
-      p2 = fma(pair(d.v, i), pair(h.v, i), p2);
+      p1 = add(p1, d.p[i]);
+      p2 = fma(d.p[i], h.p[i], p2);
     }
-    const Vec<2> s = sum(Vec<2>{{total(p1), total(p2)}}, slot);
-    const float s1 = layer ? s.v[0] * -inv_d : 0.0f, s2 = s.v[1] * -inv_d;
+    const Vec<2> s = sum(two(total(p1), total(p2)), slot);
+    const float s1 = layer ? s[0] * -inv_d : 0.0f, s2 = s[1] * -inv_d;
 #pragma unroll
     for (int i = 0; i < R::P; ++i)
-      set_pair(d.v, i,
-               mul(all<2>(r), fma(pair(h.v, i), all<2>(s2), add(pair(d.v, i), all<2>(s1)))));
+      d.p[i] = mul(all<2>(r), fma(h.p[i], all<2>(s2), add(d.p[i], all<2>(s1))));
     if (layer) d.clear_rest(lane, nv);
   }
   // v <- v (.) w
@@ -379,8 +377,8 @@ template <typename G> struct Block {
         for (int j = 0; j < G::kV; j += 4) {
           const float4 f = *reinterpret_cast<const float4*>(w + i * G::kV + j);
           const int k = (c * G::kV + j) / 2;
-          set_pair(v.v, k, mul(pair(v.v, k), Vec<2>{{f.x, f.y}}));
-          set_pair(v.v, k + 1, mul(pair(v.v, k + 1), Vec<2>{{f.z, f.w}}));
+          v.p[k] = mul(v.p[k], two(f.x, f.y));
+          v.p[k + 1] = mul(v.p[k + 1], two(f.z, f.w));
         }
       }
     }
@@ -443,7 +441,7 @@ add_norm_ring_backward(AddNormArgs a, float* part_w, float* part_post, int stage
   const float inv_d = 1.0f / a.d;
   R acc_w, acc_post;
 #pragma unroll
-  for (int i = 0; i < R::E; ++i) acc_w.v[i] = acc_post.v[i] = 0.0f;
+  for (int i = 0; i < R::P; ++i) acc_w.p[i] = acc_post.p[i] = all<2>(0.0f);
   int s = 0, phase = 0;
   for (long long n = blockIdx.x; n < a.rows; n += gridDim.x) {
     sm100::mbar_wait(&full[s], phase, kSiteRing + 1);
@@ -460,8 +458,8 @@ add_norm_ring_backward(AddNormArgs a, float* part_w, float* part_post, int stage
     }
     load(h, 0);
     const float2 mine_h = B::own(h, layer, lane, nv);
-    const Vec<2> m2 = warp_sum(Vec<2>{{mine_h.y, mine_x.y}});
-    if (lane % 32 == 0) moments[lane / 32] = make_float4(mine_h.x, m2.v[0], mine_x.x, m2.v[1]);
+    const Vec<2> m2 = warp_sum(two(mine_h.y, mine_x.y));
+    if (lane % 32 == 0) moments[lane / 32] = make_float4(mine_h.x, m2[0], mine_x.x, m2[1]);
     B::sync();
     const Moments mh = B::join(
         [&](int i) { return make_float2(moments[i].x, moments[i].y); }, layer, a.eps, inv_d, nv);
@@ -478,7 +476,7 @@ add_norm_ring_backward(AddNormArgs a, float* part_w, float* part_post, int stage
     if (a.d_res_out) {
       load(h, 2 * row);
 #pragma unroll
-      for (int i = 0; i < R::P; ++i) set_pair(d.v, i, add(pair(d.v, i), pair(h.v, i)));
+      for (int i = 0; i < R::P; ++i) d.p[i] = add(d.p[i], h.p[i]);
     }
     if (a.grad_residual) {
       h = d;

@@ -86,7 +86,7 @@ norm_gate_rows(const T* y, const T* gate, T* o, int H, int N, int dv, bool layer
     z.normalise(lane, take, layer, eps, inv_d, [](float x, int) { return row_sum<TPR>(x); });
     if constexpr (GATE) {
 #pragma unroll
-      for (int k = 0; k < R::P; ++k) set_pair(z.v, k, mul(pair(z.v, k), swish(pair(g.v, k))));
+      for (int k = 0; k < R::P; ++k) z.p[k] = mul(z.p[k], swish(g.p[k]));
     }
     z.store(o, lane, take);
     y += step, o += step_o;
@@ -127,14 +127,14 @@ norm_gate_rows_backward(const T* y, const T* gate, const T* d_o, T* grad_y, T* g
     Vec<2> p1 = all<2>(0.0f), p2 = p1;
 #pragma unroll
     for (int k = 0; k < R::P; ++k) {
-      Vec<2> dk = pair(d.v, k);
-      const Vec<2> zk = pair(z.v, k);
+      Vec<2> dk = d.p[k];
+      const Vec<2> zk = z.p[k];
       if constexpr (GATE) {
         Vec<2> sw, slope;
-        swish_grad(pair(g.v, k), &sw, &slope);
-        set_pair(g.v, k, mul(mul(dk, zk), slope));
+        swish_grad(g.p[k], &sw, &slope);
+        g.p[k] = mul(mul(dk, zk), slope);
         dk = mul(dk, sw);
-        set_pair(d.v, k, dk);
+        d.p[k] = dk;
       }
       p1 = add(p1, dk);
       p2 = fma(dk, zk, p2);
@@ -144,8 +144,7 @@ norm_gate_rows_backward(const T* y, const T* gate, const T* d_o, T* grad_y, T* g
     const float s2 = row_sum<TPR>(total(p2)) * -inv_d;
 #pragma unroll
     for (int k = 0; k < R::P; ++k)
-      set_pair(z.v, k,
-               mul(all<2>(r), fma(pair(z.v, k), all<2>(s2), add(pair(d.v, k), all<2>(s1)))));
+      z.p[k] = mul(all<2>(r), fma(z.p[k], all<2>(s2), add(d.p[k], all<2>(s1))));
     z.store(grad_y, lane, take);
     y += step, grad_y += step, d_o += step_o;
     if constexpr (GATE) gate += step_g, grad_gate += step_gg;

@@ -41,59 +41,67 @@ template <int I> struct Int { static constexpr int value = I; };
 // At 6.5 TB/s an SM has about 31 instruction slots per lane for an element of
 // which 6 bytes move: the kernels below stay under that only with pairs and
 // with the plain hardware exponential and reciprocal.
-template <int n> struct Vec {
-  float v[n];
+// A pair is one 64-bit register: held as two floats and packed at every
+// operation it would cost moves (a third of the instructions of the kernels
+// below when it was so).
+template <int n> struct Vec;
+template <> struct Vec<1> {
+  float a;
+  __device__ __forceinline__ float operator[](int) const { return a; }
 };
-template <int n> __device__ __forceinline__ Vec<n> all(float x) {
-  Vec<n> r;
-#pragma unroll
-  for (int i = 0; i < n; ++i) r.v[i] = x;
+template <> struct Vec<2> {
+  unsigned long long ab;
+  __device__ __forceinline__ float operator[](int i) const {
+    return __uint_as_float(static_cast<uint32_t>(i ? ab >> 32 : ab));
+  }
+};
+__device__ __forceinline__ Vec<2> two(float a, float b) {
+  Vec<2> r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.ab) : "f"(a), "f"(b));
   return r;
 }
+__device__ __forceinline__ Vec<1> vec(const float (&x)[1]) { return {x[0]}; }
+__device__ __forceinline__ Vec<2> vec(const float (&x)[2]) { return two(x[0], x[1]); }
+template <int n> __device__ __forceinline__ Vec<n> all(float x) {
+  float v[n];
+#pragma unroll
+  for (int i = 0; i < n; ++i) v[i] = x;
+  return vec(v);
+}
 __device__ __forceinline__ Vec<1> fma(Vec<1> a, Vec<1> b, Vec<1> c) {
-  return {{fmaf(a.v[0], b.v[0], c.v[0])}};
+  return {fmaf(a.a, b.a, c.a)};
 }
 __device__ __forceinline__ Vec<2> fma(Vec<2> a, Vec<2> b, Vec<2> c) {
   Vec<2> r;
-  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(r.v[0]), "=f"(r.v[1])
-      : "f"(a.v[0]), "f"(a.v[1]), "f"(b.v[0]), "f"(b.v[1]), "f"(c.v[0]), "f"(c.v[1]));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.ab) : "l"(a.ab), "l"(b.ab), "l"(c.ab));
   return r;
 }
-__device__ __forceinline__ Vec<1> add(Vec<1> a, Vec<1> b) { return {{a.v[0] + b.v[0]}}; }
+__device__ __forceinline__ Vec<1> add(Vec<1> a, Vec<1> b) { return {a.a + b.a}; }
 __device__ __forceinline__ Vec<2> add(Vec<2> a, Vec<2> b) {
   Vec<2> r;
-  asm("{\n\t.reg .b64 a, b, d;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(r.v[0]), "=f"(r.v[1])
-      : "f"(a.v[0]), "f"(a.v[1]), "f"(b.v[0]), "f"(b.v[1]));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.ab) : "l"(a.ab), "l"(b.ab));
   return r;
 }
-__device__ __forceinline__ Vec<1> mul(Vec<1> a, Vec<1> b) { return {{a.v[0] * b.v[0]}}; }
+__device__ __forceinline__ Vec<1> mul(Vec<1> a, Vec<1> b) { return {a.a * b.a}; }
 __device__ __forceinline__ Vec<2> mul(Vec<2> a, Vec<2> b) {
   Vec<2> r;
-  asm("{\n\t.reg .b64 a, b, d;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(r.v[0]), "=f"(r.v[1])
-      : "f"(a.v[0]), "f"(a.v[1]), "f"(b.v[0]), "f"(b.v[1]));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.ab) : "l"(a.ab), "l"(b.ab));
   return r;
 }
 
 // 2^x and 1/x by the hardware's approximations (2 and 1 units in the last
 // place); 1/x of an infinity is 0.
 template <int n> __device__ __forceinline__ Vec<n> exp2v(Vec<n> x) {
+  float y[n];
 #pragma unroll
-  for (int i = 0; i < n; ++i) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x.v[i]) : "f"(x.v[i]));
-  return x;
+  for (int i = 0; i < n; ++i) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y[i]) : "f"(x[i]));
+  return vec(y);
 }
 template <int n> __device__ __forceinline__ Vec<n> rcpv(Vec<n> x) {
+  float y[n];
 #pragma unroll
-  for (int i = 0; i < n; ++i) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(x.v[i]) : "f"(x.v[i]));
-  return x;
+  for (int i = 0; i < n; ++i) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y[i]) : "f"(x[i]));
+  return vec(y);
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -111,29 +119,27 @@ __device__ __forceinline__ void swish_grad(Vec<n> g, Vec<n>* sw, Vec<n>* slope) 
   *slope = fma(*sw, fma(s, all<n>(-1.0f), all<n>(1.0f)), s);
 }
 
-// E values of a row in one thread's registers, handled in pairs.
-template <int E> __device__ __forceinline__ Vec<2> pair(const float (&v)[E], int i) {
-  return {{v[2 * i], v[2 * i + 1]}};
-}
-template <int E> __device__ __forceinline__ void set_pair(float (&v)[E], int i, Vec<2> x) {
-  v[2 * i] = x.v[0], v[2 * i + 1] = x.v[1];
-}
-__device__ __forceinline__ float total(Vec<2> x) { return x.v[0] + x.v[1]; }
+__device__ __forceinline__ float total(Vec<2> x) { return x[0] + x[1]; }
 
 // One thread's part of a row of d = nv V elements: CH accesses of V elements,
 // TPR threads apart.  Elements past d are zeros.
 template <typename T, int V, int CH, int TPR> struct RowPart {
   static constexpr int E = CH * V, P = E / 2;
   static_assert(E % 2 == 0, "handled in pairs");
-  float v[E];
+  Vec<2> p[P];
+  __device__ __forceinline__ float get(int e) const { return p[e / 2][e % 2]; }
+  __device__ __forceinline__ void put(int e, float x) {
+    p[e / 2] = e % 2 ? two(p[e / 2][0], x) : two(x, p[e / 2][1]);
+  }
   // `nv` is 0 for a thread whose row does not exist
-  __device__ __forceinline__ void load(const T* p, int lane, int nv) {
+  __device__ __forceinline__ void load(const T* from, int lane, int nv) {
+    float v[E];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int i = c * TPR + lane;
       float x[V];
       if (i < nv) {
-        load_pack<T, V>(p + (long long)i * V, x);
+        load_pack<T, V>(from + (long long)i * V, x);
       } else {
 #pragma unroll
         for (int k = 0; k < V; ++k) x[k] = 0.0f;
@@ -141,16 +147,18 @@ template <typename T, int V, int CH, int TPR> struct RowPart {
 #pragma unroll
       for (int k = 0; k < V; ++k) v[c * V + k] = x[k];
     }
+#pragma unroll
+    for (int i = 0; i < P; ++i) p[i] = two(v[2 * i], v[2 * i + 1]);
   }
   template <typename S>  // stores to another element type share the layout
-  __device__ __forceinline__ void store(S* p, int lane, int nv) const {
+  __device__ __forceinline__ void store(S* to, int lane, int nv) const {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int i = c * TPR + lane;
       float x[V];
 #pragma unroll
-      for (int k = 0; k < V; ++k) x[k] = v[c * V + k];
-      if (i < nv) store_pack<S, V>(p + (long long)i * V, x);
+      for (int k = 0; k < V; ++k) x[k] = get(c * V + k);
+      if (i < nv) store_pack<S, V>(to + (long long)i * V, x);
     }
   }
   // Zeros past d again.
@@ -160,7 +168,7 @@ template <typename T, int V, int CH, int TPR> struct RowPart {
     for (int c = 0; c < CH; ++c)
       if (c * TPR + lane >= nv) {
 #pragma unroll
-        for (int k = 0; k < V; ++k) v[c * V + k] = 0.0f;
+        for (int k = 0; k < V; ++k) put(c * V + k, 0.0f);
       }
   }
   // v <- (v - [mean]) r, r = 1 / sqrt(mean square + eps); returns r.  sum(x)
@@ -171,19 +179,19 @@ template <typename T, int V, int CH, int TPR> struct RowPart {
     if (layer) {
       Vec<2> s = all<2>(0.0f);
 #pragma unroll
-      for (int i = 0; i < P; ++i) s = add(s, pair(v, i));
+      for (int i = 0; i < P; ++i) s = add(s, p[i]);
       const Vec<2> less = all<2>(-sum(total(s), 0) * inv_d);
 #pragma unroll
-      for (int i = 0; i < P; ++i) set_pair(v, i, add(pair(v, i), less));
+      for (int i = 0; i < P; ++i) p[i] = add(p[i], less);
       clear_rest(lane, nv);
     }
     Vec<2> q = all<2>(0.0f);
 #pragma unroll
-    for (int i = 0; i < P; ++i) q = fma(pair(v, i), pair(v, i), q);
+    for (int i = 0; i < P; ++i) q = fma(p[i], p[i], q);
     const float square = sum(total(q), 1);
     const float r = nv > 0 ? rsqrtf(fmaf(square, inv_d, eps)) : 0.0f;
 #pragma unroll
-    for (int i = 0; i < P; ++i) set_pair(v, i, mul(pair(v, i), all<2>(r)));
+    for (int i = 0; i < P; ++i) p[i] = mul(p[i], all<2>(r));
     return r;
   }
 };

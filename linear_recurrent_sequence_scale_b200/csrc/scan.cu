@@ -39,10 +39,11 @@ template <int FORM, int n> __device__ __forceinline__ Vec<n> less_one(Vec<n> f) 
     s = fma(f, s, all<n>(0.5f));
     s = fma(f, s, all<n>(1.0f));
     s = mul(f, s);
-    Vec<n> q = add(e, all<n>(-1.0f));
+    const Vec<n> q = add(e, all<n>(-1.0f));
+    float pick[n];
 #pragma unroll
-    for (int i = 0; i < n; ++i) q.v[i] = fabsf(f.v[i]) < 0.25f ? s.v[i] : q.v[i];
-    return q;
+    for (int i = 0; i < n; ++i) pick[i] = fabsf(f[i]) < 0.25f ? s[i] : q[i];
+    return vec(pick);
   }
 }
 
@@ -130,48 +131,52 @@ __device__ __forceinline__ float word(float x) {
 template <int n> __device__ __forceinline__ bool written(const Vec<n>& x) {
   bool r = true;
 #pragma unroll
-  for (int i = 0; i < n; ++i) r = r && __float_as_uint(x.v[i]) != kEmpty;
+  for (int i = 0; i < n; ++i) r = r && __float_as_uint(x[i]) != kEmpty;
   return r;
 }
 // Words are read and written one by one as far as their meaning goes; the
 // vector forms only save instructions.
 __device__ __forceinline__ void ld_words(const float* p, Vec<1>& a) {
-  asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(a.v[0]) : "l"(p) : "memory");
+  asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(a.a) : "l"(p) : "memory");
 }
 __device__ __forceinline__ void ld_words(const float* p, Vec<2>& a) {
+  float x, y;
   asm volatile("ld.relaxed.gpu.global.v2.f32 {%0, %1}, [%2];"
-               : "=f"(a.v[0]), "=f"(a.v[1])
+               : "=f"(x), "=f"(y)
                : "l"(p)
                : "memory");
+  a = two(x, y);
 }
 __device__ __forceinline__ void ld_words(const float* p, Vec<1>& a, Vec<1>& b) {
   asm volatile("ld.relaxed.gpu.global.v2.f32 {%0, %1}, [%2];"
-               : "=f"(a.v[0]), "=f"(b.v[0])
+               : "=f"(a.a), "=f"(b.a)
                : "l"(p)
                : "memory");
 }
 __device__ __forceinline__ void ld_words(const float* p, Vec<2>& a, Vec<2>& b) {
+  float x, y, z, w;
   asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(a.v[0]), "=f"(a.v[1]), "=f"(b.v[0]), "=f"(b.v[1])
+               : "=f"(x), "=f"(y), "=f"(z), "=f"(w)
                : "l"(p)
                : "memory");
+  a = two(x, y), b = two(z, w);
 }
 __device__ __forceinline__ void st_words(float* p, Vec<1> a) {
-  asm volatile("st.relaxed.gpu.global.f32 [%0], %1;" ::"l"(p), "f"(word(a.v[0])) : "memory");
+  asm volatile("st.relaxed.gpu.global.f32 [%0], %1;" ::"l"(p), "f"(word(a.a)) : "memory");
 }
 __device__ __forceinline__ void st_words(float* p, Vec<2> a) {
-  asm volatile("st.relaxed.gpu.global.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(word(a.v[0])),
-               "f"(word(a.v[1]))
+  asm volatile("st.relaxed.gpu.global.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(word(a[0])),
+               "f"(word(a[1]))
                : "memory");
 }
 __device__ __forceinline__ void st_words(float* p, Vec<1> a, Vec<1> b) {
-  asm volatile("st.relaxed.gpu.global.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(word(a.v[0])),
-               "f"(word(b.v[0]))
+  asm volatile("st.relaxed.gpu.global.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(word(a.a)),
+               "f"(word(b.a))
                : "memory");
 }
 __device__ __forceinline__ void st_words(float* p, Vec<2> a, Vec<2> b) {
-  asm volatile("st.relaxed.gpu.global.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p),
-               "f"(word(a.v[0])), "f"(word(a.v[1])), "f"(word(b.v[0])), "f"(word(b.v[1]))
+  asm volatile("st.relaxed.gpu.global.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(word(a[0])),
+               "f"(word(a[1])), "f"(word(b[0])), "f"(word(b[1]))
                : "memory");
 }
 
@@ -292,39 +297,46 @@ __device__ __forceinline__ void compute_sync() {
 // The channels of one lane: 4 bytes of a row.
 template <typename T> constexpr int kLane = 4 / sizeof(T);
 template <typename T> __device__ __forceinline__ Vec<kLane<T>> get(const char* row) {
-  Vec<kLane<T>> r;
-  load_pack<T, kLane<T>>(reinterpret_cast<const T*>(row) + (threadIdx.x % 32) * kLane<T>, r.v);
-  return r;
+  float r[kLane<T>];
+  load_pack<T, kLane<T>>(reinterpret_cast<const T*>(row) + (threadIdx.x % 32) * kLane<T>, r);
+  return vec(r);
 }
 template <typename T, int n> __device__ __forceinline__ void set(char* row, const Vec<n>& x) {
-  store_pack<T, n>(reinterpret_cast<T*>(row) + (threadIdx.x % 32) * n, x.v);
+  float v[n];
+#pragma unroll
+  for (int i = 0; i < n; ++i) v[i] = x[i];
+  store_pack<T, n>(reinterpret_cast<T*>(row) + (threadIdx.x % 32) * n, v);
 }
 // `left`: channels of the piece that exist from this lane's first one on.
 template <typename T, bool PAIR, int n>
 __device__ __forceinline__ void put(T* p, const Vec<n>& x, int left) {
+  float v[n];
+#pragma unroll
+  for (int i = 0; i < n; ++i) v[i] = x[i];
   if (PAIR || n == 1) {
-    if (left > 0) store_pack<T, n>(p, x.v);
+    if (left > 0) store_pack<T, n>(p, v);
   } else {
 #pragma unroll
     for (int i = 0; i < n; ++i)
-      if (i < left) Elem<T>::st(p + i, x.v[i]);
+      if (i < left) Elem<T>::st(p + i, v[i]);
   }
 }
 template <int n> __device__ __forceinline__ Vec<n> get_state(const float* p, int left) {
-  Vec<n> r;
+  float r[n];
 #pragma unroll
-  for (int i = 0; i < n; ++i) r.v[i] = p && i < left ? p[i] : 0.0f;
-  return r;
+  for (int i = 0; i < n; ++i) r[i] = p && i < left ? p[i] : 0.0f;
+  return vec(r);
 }
 template <int n> __device__ __forceinline__ void put_state(float* p, const Vec<n>& x, int left) {
 #pragma unroll
   for (int i = 0; i < n; ++i)
-    if (i < left) p[i] = x.v[i];
+    if (i < left) p[i] = x[i];
 }
 template <int FORM, int n> __device__ __forceinline__ Vec<n> turn(Vec<n> h) {
+  float r[n];
 #pragma unroll
-  for (int i = 0; i < n; ++i) h.v[i] = turn<FORM>(h.v[i]);
-  return h;
+  for (int i = 0; i < n; ++i) r[i] = turn<FORM>(h[i]);
+  return vec(r);
 }
 
 constexpr int kTokForward = 128, kTokBackward = RET_SCAN_CHUNK;
@@ -811,23 +823,22 @@ __global__ void __launch_bounds__(kThreads) scan_token(const ScanArgs a) {
   const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
   if (i >= (long long)a.B * per_row) return;
   const long long b = i / per_row, d = (i - b * per_row) * V;
-  Vec<V> z, f, x;
-  load_pack<float, V>(a.state_in + b * a.D + d, z.v);
-  load_pack<T, V>(at<T>(a.f, b, 0, d), f.v);
-  load_pack<T, V>(at<T>(a.x, b, 0, d), x.v);
-  Vec<V> g;
-  if constexpr (GATE) load_pack<T, V>(at<T>(a.gate, b, 0, d), g.v);
+  float z[V], f[V], x[V], g[V];
+  load_pack<float, V>(a.state_in + b * a.D + d, z);
+  load_pack<T, V>(at<T>(a.f, b, 0, d), f);
+  load_pack<T, V>(at<T>(a.x, b, 0, d), x);
+  if constexpr (GATE) load_pack<T, V>(at<T>(a.gate, b, 0, d), g);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const Vec<1> q = less_one<FORM>(Vec<1>{{f.v[v]}});
-    z.v[v] = turn<FORM>(advance<FORM>(Vec<1>{{turn<FORM>(z.v[v])}}, q, Vec<1>{{x.v[v]}}).v[0]);
+    const Vec<1> q = less_one<FORM>(Vec<1>{f[v]});
+    z[v] = turn<FORM>(advance<FORM>(Vec<1>{turn<FORM>(z[v])}, q, Vec<1>{x[v]}).a);
   }
-  store_pack<float, V>(a.state_out + b * a.D + d, z.v);
+  store_pack<float, V>(a.state_out + b * a.D + d, z);
   if constexpr (GATE) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) z.v[v] *= swish(Vec<1>{{g.v[v]}}).v[0];
+    for (int v = 0; v < V; ++v) z[v] *= swish(Vec<1>{g[v]}).a;
   }
-  store_pack<T, V>(at<T>(a.y, b, 0, d), z.v);
+  store_pack<T, V>(at<T>(a.y, b, 0, d), z);
 }
 
 // Calls fn with the element type, the form and whether there is a gate as
