@@ -52,8 +52,10 @@ template <int TPR> __device__ __forceinline__ float row_sum(float a, float2* slo
 }
 
 // Row geometry: CH accesses of V elements per thread and tensor.
-template <typename T, int V, int CH, int TPR> struct Geo {
+template <typename T, int V, int CH, int TPR, bool FULL = false> struct Geo {
   using type = T;
+  using Full = Geo<T, V, CH, TPR, true>;  // for rows of exactly CH V TPR elements
+  static constexpr bool kFull = FULL;
   static constexpr int kV = V, kCH = CH, kTPR = TPR;
   static constexpr int kThreads = TPR < 128 ? 128 : TPR;  // several short rows per block
   static constexpr int kRows = kThreads / TPR;
@@ -61,9 +63,9 @@ template <typename T, int V, int CH, int TPR> struct Geo {
 };
 
 template <typename G>
-struct Row : RowPart<typename G::type, G::kV, G::kCH, G::kTPR> {
+struct Row : RowPart<typename G::type, G::kV, G::kCH, G::kTPR, G::kFull> {
   static constexpr int V = G::kV, CH = G::kCH, TPR = G::kTPR;
-  using Base = RowPart<typename G::type, V, CH, TPR>;
+  using Base = RowPart<typename G::type, V, CH, TPR, G::kFull>;
   using Base::P;
   using Base::p;
   // v <- v (.) w
@@ -282,7 +284,7 @@ template <typename G> struct Block {
       Vec<2> s = all<2>(0.0f);
 #pragma unroll
       for (int i = 0; i < R::P; ++i) s = add(s, v.p[i]);
-      const int n = nv == G::kCH * G::kTPR ? 32 * kLane : held(lane / 32, nv);
+      const int n = G::kFull ? 32 * kLane : held(lane / 32, nv);
       const float sum = warp_sum(total(s));
       mean = n > 0 ? __fdividef(sum, (float)n) : 0.0f;
     }
@@ -308,7 +310,7 @@ template <typename G> struct Block {
     if (!layer) {
 #pragma unroll
       for (int w = 0; w < W; ++w) m2 += get(w).y;
-    } else if (nv == G::kCH * G::kTPR) {  // every warp holds as much
+    } else if (G::kFull) {  // every warp holds as much
       float apart = 0.0f;
 #pragma unroll
       for (int w = 0; w < W; ++w) mean += get(w).x;
@@ -372,7 +374,7 @@ template <typename G> struct Block {
 #pragma unroll
     for (int c = 0; c < G::kCH; ++c) {
       const int i = c * G::kTPR + lane;
-      if (i < nv) {
+      if (G::kFull || i < nv) {
 #pragma unroll
         for (int j = 0; j < G::kV; j += 4) {
           const float4 f = *reinterpret_cast<const float4*>(w + i * G::kV + j);
@@ -615,11 +617,12 @@ cudaError_t launch_add_norm_backward(const AddNormArgs& a, float* ws, cudaStream
     cudaError_t e = cudaSuccess;
     if constexpr (G::kTPR > 32 && G::kTPR <= 512 && G::kV > 1) {
       if (stages) {
-        e = cudaFuncSetAttribute(an::add_norm_ring_backward<G>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        const auto kernel = a.d == G::kCH * G::kV * G::kTPR
+                                ? an::add_norm_ring_backward<typename G::Full>
+                                : an::add_norm_ring_backward<G>;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        an::add_norm_ring_backward<G>
-            <<<grid, G::kTPR + 32, smem, st>>>(a, part_w, part_post, stages);
+        kernel<<<grid, G::kTPR + 32, smem, st>>>(a, part_w, part_post, stages);
       }
     }
     if (!stages) an::add_norm_rows_backward<G><<<grid, G::kThreads, 0, st>>>(a, part_w, part_post);

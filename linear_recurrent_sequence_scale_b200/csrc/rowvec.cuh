@@ -122,8 +122,9 @@ __device__ __forceinline__ void swish_grad(Vec<n> g, Vec<n>* sw, Vec<n>* slope) 
 __device__ __forceinline__ float total(Vec<2> x) { return x[0] + x[1]; }
 
 // One thread's part of a row of d = nv V elements: CH accesses of V elements,
-// TPR threads apart.  Elements past d are zeros.
-template <typename T, int V, int CH, int TPR> struct RowPart {
+// TPR threads apart.  Elements past d are zeros.  FULL: there are none (d =
+// CH V TPR, and the row exists), which spares the zeros and the comparisons.
+template <typename T, int V, int CH, int TPR, bool FULL = false> struct RowPart {
   static constexpr int E = CH * V, P = E / 2;
   static_assert(E % 2 == 0, "handled in pairs");
   Vec<2> p[P];
@@ -138,8 +139,8 @@ template <typename T, int V, int CH, int TPR> struct RowPart {
     for (int c = 0; c < CH; ++c) {
       const int i = c * TPR + lane;
       float x[V];
-      if (i < nv) {
-        load_pack<T, V>(from + (long long)i * V, x);
+      if (FULL || i < nv) {
+        load_pack<T, V>(from + i * V, x);
       } else {
 #pragma unroll
         for (int k = 0; k < V; ++k) x[k] = 0.0f;
@@ -158,12 +159,12 @@ template <typename T, int V, int CH, int TPR> struct RowPart {
       float x[V];
 #pragma unroll
       for (int k = 0; k < V; ++k) x[k] = get(c * V + k);
-      if (i < nv) store_pack<S, V>(to + (long long)i * V, x);
+      if (FULL || i < nv) store_pack<S, V>(to + i * V, x);
     }
   }
   // Zeros past d again.
   __device__ __forceinline__ void clear_rest(int lane, int nv) {
-    if (nv == CH * TPR) return;
+    if (FULL || nv == CH * TPR) return;
 #pragma unroll
     for (int c = 0; c < CH; ++c)
       if (c * TPR + lane >= nv) {
@@ -189,7 +190,7 @@ template <typename T, int V, int CH, int TPR> struct RowPart {
 #pragma unroll
     for (int i = 0; i < P; ++i) q = fma(p[i], p[i], q);
     const float square = sum(total(q), 1);
-    const float r = nv > 0 ? rsqrtf(fmaf(square, inv_d, eps)) : 0.0f;
+    const float r = FULL || nv > 0 ? rsqrtf(fmaf(square, inv_d, eps)) : 0.0f;
 #pragma unroll
     for (int i = 0; i < P; ++i) p[i] = mul(p[i], all<2>(r));
     return r;
