@@ -57,9 +57,9 @@ template <typename T, int V, int CH, int TPR, bool FULL = false> struct Geo {
   using Full = Geo<T, V, CH, TPR, true>;  // for rows of exactly CH V TPR elements
   static constexpr bool kFull = FULL;
   static constexpr int kV = V, kCH = CH, kTPR = TPR;
-  static constexpr int kThreads = TPR < 128 ? 128 : TPR;  // several short rows per block
+  static constexpr int kThreads = TPR < 64 ? 128 : TPR;  // several short rows per block
   static constexpr int kRows = kThreads / TPR;
-  static_assert(TPR <= 32 || kThreads == TPR, "the block barrier serves one row");
+  
 };
 
 template <typename G>
@@ -232,18 +232,22 @@ add_norm_rows_backward(AddNormArgs a, float* part_w, float* part_post) {
                   acc_post, part_w, part_post);
 }
 
-// The same with the rows coming through a ring in shared memory: one more
-// warp copies whole rows (each tensor's is one contiguous piece) a few rows
-// ahead, so HBM stays busy while the block waits for its row's sums.  What
-// remains is instructions (about 30 per element; HBM allows 62), so the sums
-// are few: both norms' moments cross the block in one exchange, each warp
-// taking its own about its own mean and the block joining them (Chan, Golub
-// and LeVeque's pairwise variance), and the weights wait in shared memory.
-// 65536 x 4096 in bf16, both norms and both weights: 1027 us with loads in
-// registers and five exchanges, 903 through the ring, ANB_US with three.
+// The same with the rows coming through a ring in shared memory.  A block is
+// as many groups of TPR threads as an SM holds, each working on a row of its
+// own with the next ones on their way (its first thread copies whole rows, each
+// tensor's being one contiguous piece): while one group waits for its row's
+// sums another computes.  A thread has 32 elements of a row, so the
+// sums cost few instructions per element; both norms' moments cross the group
+// in one exchange, each warp taking its own about its own mean and the group
+// joining them (Chan, Golub and LeVeque's pairwise variance); and the weights
+// wait in shared memory.  65536 x 4096 in bf16, both norms and both weights:
+// 1027 us with loads in registers and five exchanges, 670 through rings of
+// two blocks per SM with 16 elements per thread, ANB_US with three groups of
+// 128 threads.
 constexpr int kSiteRing = 811;
 constexpr int kMaxStages = 4;
-template <int THREADS> constexpr int kRingBlocks = THREADS <= 128 ? 4 : THREADS <= 256 ? 2 : 1;
+constexpr int kRingWarps = 12;  // three on each scheduler: 168 registers a thread
+constexpr int kRingBytes = 225 * 1024;  // beside 1 KB of barriers and sums
 
 __device__ __forceinline__ Vec<2> warp_sum(Vec<2> x) {
 #pragma unroll
@@ -266,8 +270,12 @@ struct Moments {
 template <typename G> struct Block {
   static constexpr int W = G::kTPR / 32;
   static constexpr int kLane = G::kCH * G::kV;  // elements of a thread in a full row
-  static __device__ __forceinline__ void sync() {
-    asm volatile("bar.sync 1, %0;" ::"n"(G::kTPR) : "memory");
+  // The group's barrier; a warp by itself needs its memory ordered only.
+  static __device__ __forceinline__ void sync(int group) {
+    if constexpr (W == 1)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(G::kTPR) : "memory");
   }
   // Elements of the row that warp w holds.
   static __device__ __forceinline__ int held(int w, int nv) {
@@ -331,18 +339,20 @@ template <typename G> struct Block {
     }
     return {mean, rsqrtf(fmaf(m2, inv_d, eps))};
   }
-  // Both sums over the block.
-  static __device__ __forceinline__ Vec<2> sum(Vec<2> x, float2* slot) {
+  // Both sums over the group.
+  static __device__ __forceinline__ Vec<2> sum(Vec<2> x, float2* slot, int group, int lane) {
     x = warp_sum(x);
-    if (threadIdx.x % 32 == 0) slot[threadIdx.x / 32] = make_float2(x[0], x[1]);
-    sync();
-    Vec<2> s = all<2>(0.0f);
+    if constexpr (W > 1) {
+      if (lane % 32 == 0) slot[lane / 32] = make_float2(x[0], x[1]);
+      sync(group);
+      x = all<2>(0.0f);
 #pragma unroll
-    for (int w = 0; w < W; w += 2) {
-      const float4 f = *reinterpret_cast<const float4*>(slot + w);
-      s = add(s, add(two(f.x, f.y), two(f.z, f.w)));
+      for (int w = 0; w < W; w += 2) {
+        const float4 f = *reinterpret_cast<const float4*>(slot + w);
+        x = add(x, add(two(f.x, f.y), two(f.z, f.w)));
+      }
     }
-    return s;
+    return x;
   }
   // v <- (v - mean) r
   static __device__ __forceinline__ void apply(Row<G>& v, Moments m, bool layer, int lane,
@@ -354,7 +364,8 @@ template <typename G> struct Block {
   }
   // d <- r (d - [mean(d)] - h mean(d (.) h))
   static __device__ __forceinline__ void back(Row<G>& d, const Row<G>& h, float r, bool layer,
-                                              float inv_d, float2* slot, int lane, int nv) {
+                                              float inv_d, float2* slot, int group, int lane,
+                                              int nv) {
     using R = Row<G>;
     Vec<2> p1 = all<2>(0.0f), p2 = p1;
 #pragma unroll
@@ -362,7 +373,7 @@ template <typename G> struct Block {
       p1 = add(p1, d.p[i]);
       p2 = fma(d.p[i], h.p[i], p2);
     }
-    const Vec<2> s = sum(two(total(p1), total(p2)), slot);
+    const Vec<2> s = sum(two(total(p1), total(p2)), slot, group, lane);
     const float s1 = layer ? s[0] * -inv_d : 0.0f, s2 = s[1] * -inv_d;
 #pragma unroll
     for (int i = 0; i < R::P; ++i)
@@ -388,118 +399,136 @@ template <typename G> struct Block {
 };
 
 template <typename G>
-__global__ void __launch_bounds__(G::kTPR + 32, kRingBlocks<G::kTPR>)
-add_norm_ring_backward(AddNormArgs a, float* part_w, float* part_post, int stages) {
+__global__ void __launch_bounds__(32 * kRingWarps, 1)
+add_norm_ring_backward(AddNormArgs a, float* part_w, float* part_post, int groups, int stages) {
   using T = typename G::type;
   using R = Row<G>;
   using B = Block<G>;
+  constexpr int kMaxGroups = kRingWarps / B::W;
   extern __shared__ __align__(128) char ring[];
-  __shared__ float4 moments[B::W];
-  __shared__ __align__(16) float2 slots[2][B::W];
-  __shared__ uint64_t full[kMaxStages], empty[kMaxStages];
+  __shared__ float4 moments[kMaxGroups][B::W];
+  __shared__ __align__(16) float2 slots[kMaxGroups][2][B::W];
+  __shared__ uint64_t full[kMaxGroups][kMaxStages];
   const bool post = a.post_norm != RET_NORM_NONE, need_x = post || part_post;
   const bool layer = a.norm == RET_NORM_LAYER, layer_post = a.post_norm == RET_NORM_LAYER;
   const uint32_t row = a.d * (uint32_t)sizeof(T);
   const uint32_t stage = row * (2 + (a.d_res_out ? 1 : 0) + (need_x ? 1 : 0));
-  // behind the ring, the weights
-  float* w = reinterpret_cast<float*>(ring + stages * stage);
+  // behind the groups' rings, the weights
+  float* w = reinterpret_cast<float*>(ring + groups * stages * stage);
   float* w_post = w + (a.w ? a.d : 0);
   if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) {
-      sm100::mbar_init(&full[s], 1);
-      sm100::mbar_init(&empty[s], B::W);
-    }
+    for (int g = 0; g < groups; ++g)
+      for (int s = 0; s < stages; ++s) sm100::mbar_init(&full[g][s], 1);
     sm100::fence_mbar_init();
   }
-  for (int i = threadIdx.x; i < a.d; i += G::kTPR + 32) {
+  for (int i = threadIdx.x; i < a.d; i += blockDim.x) {
     if (a.w) w[i] = a.w[i];
     if (a.w_post) w_post[i] = a.w_post[i];
   }
   __syncthreads();
-  const int lane = threadIdx.x, nv = a.d / G::kV;
-  if (threadIdx.x >= G::kTPR) {
-    if (threadIdx.x > G::kTPR) return;
-    int s = 0, phase = 0;
-    bool first = true;
-    for (long long n = blockIdx.x; n < a.rows; n += gridDim.x) {
-      if (!first && !sm100::mbar_wait(&empty[s], phase ^ 1, kSiteRing)) {
-        for (int i = 0; i < stages; ++i)  // the copies under way end before the block does
-          sm100::mbar_drain(&full[i], i < s ? phase : phase ^ 1);
-        return;
-      }
-      const auto load = [&](const void* p, uint32_t place) {
-        sm100::bulk_load(ring + s * stage + place, static_cast<const T*>(p) + n * a.d, row,
-                         &full[s]);
-      };
-      sm100::mbar_arrive_expect_tx(&full[s], stage);
-      load(a.res_out, 0);
-      load(a.d_y, row);
-      if (a.d_res_out) load(a.d_res_out, 2 * row);
-      if (need_x) load(a.x, stage - row);
-      if (++s == stages) s = 0, phase ^= 1, first = false;
-    }
-    return;
-  }
-  const float inv_d = 1.0f / a.d;
+  const int group = threadIdx.x / G::kTPR, lane = threadIdx.x % G::kTPR, nv = a.d / G::kV;
+  const long long first = (long long)blockIdx.x * groups, step = (long long)gridDim.x * groups;
   R acc_w, acc_post;
 #pragma unroll
   for (int i = 0; i < R::P; ++i) acc_w.p[i] = acc_post.p[i] = all<2>(0.0f);
-  int s = 0, phase = 0;
-  for (long long n = blockIdx.x; n < a.rows; n += gridDim.x) {
-    sm100::mbar_wait(&full[s], phase, kSiteRing + 1);
-    const auto load = [&](R& part, uint32_t place) {
-      part.load(reinterpret_cast<const T*>(ring + s * stage + place), lane, nv);
+  // by the group's first thread: row n into stage s
+  const auto fetch = [&](long long n, int s) {
+    if (n >= a.rows) return;
+    char* to = ring + (group * stages + s) * stage;
+    const auto load = [&](const void* p, uint32_t place) {
+      sm100::bulk_load(to + place, static_cast<const T*>(p) + n * a.d, row, &full[group][s]);
     };
-    const long long at = n * a.d;
-    R h, d;
-    // both norms' moments
-    float2 mine_x = make_float2(0.0f, 0.0f);
-    if (post) {
-      load(d, stage - row);
-      mine_x = B::own(d, layer_post, lane, nv);
-    }
-    load(h, 0);
-    const float2 mine_h = B::own(h, layer, lane, nv);
-    const Vec<2> m2 = warp_sum(two(mine_h.y, mine_x.y));
-    if (lane % 32 == 0) moments[lane / 32] = make_float4(mine_h.x, m2[0], mine_x.x, m2[1]);
-    B::sync();
-    const Moments mh = B::join(
-        [&](int i) { return make_float2(moments[i].x, moments[i].y); }, layer, a.eps, inv_d, nv);
-    Moments mx = {0.0f, 1.0f};
-    if (post)
-      mx = B::join([&](int i) { return make_float2(moments[i].z, moments[i].w); }, layer_post,
-                   a.eps, inv_d, nv);
-    // through the norm before the next block
-    B::apply(h, mh, layer, lane, nv);
-    load(d, row);
-    if (part_w) acc_w.add_product(d, h);
-    if (a.w) B::scale(d, w, lane, nv);
-    B::back(d, h, mh.r, layer, inv_d, slots[0], lane, nv);
-    if (a.d_res_out) {
-      load(h, 2 * row);
+    sm100::mbar_arrive_expect_tx(&full[group][s], stage);
+    load(a.res_out, 0);
+    load(a.d_y, row);
+    if (a.d_res_out) load(a.d_res_out, 2 * row);
+    if (need_x) load(a.x, stage - row);
+  };
+  {
+    if (lane == 0)
+      for (int s = 0; s < stages; ++s) fetch(first + group + s * step, s);
+    const float inv_d = 1.0f / a.d;
+    int s = 0, phase = 0;
+    for (long long n = first + group; n < a.rows; n += step) {
+      sm100::mbar_wait(&full[group][s], phase, kSiteRing + 1);
+      const char* here = ring + (group * stages + s) * stage;
+      const auto load = [&](R& part, uint32_t place) {
+        part.load(reinterpret_cast<const T*>(here + place), lane, nv);
+      };
+      const long long at = n * a.d;
+      R h, d;
+      // both norms' moments
+      float2 mine_x = make_float2(0.0f, 0.0f);
+      if (post) {
+        load(d, stage - row);
+        mine_x = B::own(d, layer_post, lane, nv);
+      }
+      load(h, 0);
+      const float2 mine_h = B::own(h, layer, lane, nv);
+      const Vec<2> m2 = warp_sum(two(mine_h.y, mine_x.y));
+      if (lane % 32 == 0)
+        moments[group][lane / 32] = make_float4(mine_h.x, m2[0], mine_x.x, m2[1]);
+      B::sync(group);
+      const Moments mh = B::join(
+          [&](int i) { return make_float2(moments[group][i].x, moments[group][i].y); }, layer,
+          a.eps, inv_d, nv);
+      Moments mx = {0.0f, 1.0f};
+      if (post)
+        mx = B::join([&](int i) { return make_float2(moments[group][i].z, moments[group][i].w); },
+                     layer_post, a.eps, inv_d, nv);
+      if (B::W == 1) __syncwarp();  // read before the next row's are written
+      // through the norm before the next block
+      B::apply(h, mh, layer, lane, nv);
+      load(d, row);
+      if (part_w) acc_w.add_product(d, h);
+      if (a.w) B::scale(d, w, lane, nv);
+      B::back(d, h, mh.r, layer, inv_d, slots[group][0], group, lane, nv);
+      if (a.d_res_out) {
+        load(h, 2 * row);
 #pragma unroll
-      for (int i = 0; i < R::P; ++i) d.p[i] = add(d.p[i], h.p[i]);
+        for (int i = 0; i < R::P; ++i) d.p[i] = add(d.p[i], h.p[i]);
+      }
+      if (a.grad_residual) {
+        h = d;
+        h.times(a.alpha);
+        h.store(static_cast<T*>(a.grad_residual) + at, lane, nv);
+      }
+      d.times(a.beta);
+      // and through the one after the block
+      if (need_x) load(h, stage - row);
+      B::sync(group);  // the stage has been read
+      if (lane == 0) fetch(n + stages * step, s);
+      if (post) B::apply(h, mx, layer_post, lane, nv);
+      if (part_post) acc_post.add_product(d, h);
+      if (a.grad_x) {
+        if (a.w_post) B::scale(d, w_post, lane, nv);
+        if (post) B::back(d, h, mx.r, layer_post, inv_d, slots[group][1], group, lane, nv);
+        d.store(static_cast<T*>(a.grad_x) + at, lane, nv);
+      }
+      if (++s == stages) s = 0, phase ^= 1;
     }
-    if (a.grad_residual) {
-      h = d;
-      h.times(a.alpha);
-      h.store(static_cast<T*>(a.grad_residual) + at, lane, nv);
-    }
-    d.times(a.beta);
-    // and through the one after the block
-    if (need_x) load(h, stage - row);
-    __syncwarp();
-    if (lane % 32 == 0) sm100::mbar_arrive(&empty[s]);
-    if (post) B::apply(h, mx, layer_post, lane, nv);
-    if (part_post) acc_post.add_product(d, h);
-    if (a.grad_x) {
-      if (a.w_post) B::scale(d, w_post, lane, nv);
-      if (post) B::back(d, h, mx.r, layer_post, inv_d, slots[1], lane, nv);
-      d.store(static_cast<T*>(a.grad_x) + at, lane, nv);
-    }
-    if (++s == stages) s = 0, phase ^= 1;
+    // where some wait gave up, the copies still under way end before the block does
+    if (lane == 0 && sm100::failed())
+      for (int i = 0; i < stages; ++i) {
+        const long long mine = a.rows - first - group;  // rows of the group: ceil(mine / step)
+        const long long rows = mine > 0 ? (mine + step - 1) / step : 0;
+        if (rows > i) sm100::mbar_drain(&full[group][i], ((rows - 1 - i) / stages) % 2);
+      }
   }
-  put_partials<G>(a, lane, nv, blockIdx.x, acc_w, acc_post, part_w, part_post);
+  // the groups' sums, through the place of their rings, in the groups' order
+  float* sums = reinterpret_cast<float*>(ring);
+  for (int which = 0; which < 2; ++which) {
+    float* part = which ? part_post : part_w;
+    if (!part) continue;
+    __syncthreads();
+    put_partials<G>(a, lane, nv, group, which ? acc_post : acc_w, acc_w, sums, nullptr);
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.d; i += blockDim.x) {
+      float s = sums[i];
+      for (int g = 1; g < groups; ++g) s += sums[(long long)g * a.d + i];
+      part[(long long)blockIdx.x * a.d + i] = s;
+    }
+  }
 }
 
 // grad[c] = sum of the partial rows, in a fixed order: 8 warps take every
@@ -536,6 +565,7 @@ bool vectored(const AddNormArgs& a) {
 
 template <typename T, int V, int CH, typename Fn> cudaError_t by_threads(int nv, Fn fn) {
   if (nv <= 32 * CH) return fn(Geo<T, V, CH, 32>());
+  if (nv <= 64 * CH) return fn(Geo<T, V, CH, 64>());
   if (nv <= 128 * CH) return fn(Geo<T, V, CH, 128>());
   if (nv <= 256 * CH) return fn(Geo<T, V, CH, 256>());
   if (nv <= 512 * CH) return fn(Geo<T, V, CH, 512>());
@@ -557,7 +587,8 @@ template <typename Fn> cudaError_t by_geometry(const AddNormArgs& a, Fn fn) {
 
 // Blocks of the backward.  A fixed count, so that the order of the weight
 // gradients' sums does not depend on the device.
-constexpr int kMaxBlocks = 592;  // four per SM
+constexpr int kMaxBlocks = 592;   // four per SM
+constexpr int kRingBlocks = 148;  // one per SM
 
 }  // namespace an
 
@@ -581,20 +612,64 @@ cudaError_t launch_add_norm(const AddNormArgs& a, cudaStream_t st) {
 
 namespace an {
 
-// Shared memory of the ring kernel for rows of this size, and its depth; 0
-// where it does not serve: fewer than two stages fit, or rows short enough for
-// a warp.
-template <typename G> int ring_bytes(const AddNormArgs& a, int* stages) {
-  *stages = 0;
-  if (G::kTPR <= 32 || G::kTPR > 512 || G::kV == 1) return 0;
+// Shape of the ring kernel's blocks for rows of this size.
+struct RingPlan {
+  int groups = 0, stages = 0, smem = 0;  // no groups: it does not serve
+};
+template <typename G> RingPlan ring_plan(const AddNormArgs& a) {
+  RingPlan p;
   const int tensors = 2 + (a.d_res_out ? 1 : 0) +
                       (a.post_norm != RET_NORM_NONE || a.grad_w_post ? 1 : 0);
   const int stage = tensors * a.d * (int)sizeof(typename G::type);
   const int weights = a.d * 4 * ((a.w ? 1 : 0) + (a.w_post ? 1 : 0));
-  const int n = (220 * 1024 / kRingBlocks<G::kTPR> - weights) / stage;
-  if (n < 2) return 0;
-  *stages = n < kMaxStages ? n : kMaxStages;
-  return *stages * stage + weights;
+  const int fit = (kRingBytes - weights) / (2 * stage), most = kRingWarps / (G::kTPR / 32);
+  p.groups = fit < most ? fit : most;
+  if (p.groups < 1) return RingPlan();
+  p.stages = (kRingBytes - weights) / (p.groups * stage);
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  p.smem = p.groups * p.stages * stage + weights;
+  return p;
+}
+
+template <typename G>
+cudaError_t run_ring(const AddNormArgs& a, float* ws, int* parts, cudaStream_t st) {
+  const RingPlan p = ring_plan<G>(a);
+  *parts = 0;
+  if (!p.groups) return cudaSuccess;
+  const long long want = (a.rows + p.groups - 1) / p.groups;
+  const int grid = static_cast<int>(want < kRingBlocks ? want : kRingBlocks);
+  const auto kernel = a.d == G::kCH * G::kV * G::kTPR ? add_norm_ring_backward<typename G::Full>
+                                                      : add_norm_ring_backward<G>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, p.groups * G::kTPR, p.smem, st>>>(
+      a, a.grad_w ? ws : nullptr,
+      a.grad_w_post ? ws + (a.grad_w ? (size_t)grid * a.d : (size_t)0) : nullptr, p.groups,
+      p.stages);
+  *parts = grid;
+  return cudaPeekAtLastError();
+}
+
+// Rows of at least 512 bytes that split into 16-byte pieces, if two of them
+// fit; *parts stays 0 where the ring does not serve.
+cudaError_t through_ring(const AddNormArgs& a, float* ws, int* parts, cudaStream_t st) {
+  using bf16 = __nv_bfloat16;
+  *parts = 0;
+  const bool half = a.dtype == RET_BF16;
+  const int nv = a.d * (half ? 2 : 4) / 16;
+  if (!vectored(a) || nv < 32 || nv > 1024) return cudaSuccess;
+  if (half) {
+    if (nv <= 64) return run_ring<Geo<bf16, 8, 2, 32>>(a, ws, parts, st);
+    if (nv <= 128) return run_ring<Geo<bf16, 8, 4, 32>>(a, ws, parts, st);
+    if (nv <= 256) return run_ring<Geo<bf16, 8, 4, 64>>(a, ws, parts, st);
+    if (nv <= 512) return run_ring<Geo<bf16, 8, 4, 128>>(a, ws, parts, st);
+    return run_ring<Geo<bf16, 8, 4, 256>>(a, ws, parts, st);
+  }
+  if (nv <= 128) return run_ring<Geo<float, 4, 4, 32>>(a, ws, parts, st);
+  if (nv <= 256) return run_ring<Geo<float, 4, 8, 32>>(a, ws, parts, st);
+  if (nv <= 512) return run_ring<Geo<float, 4, 8, 64>>(a, ws, parts, st);
+  return run_ring<Geo<float, 4, 8, 128>>(a, ws, parts, st);
 }
 
 }  // namespace an
@@ -602,36 +677,28 @@ template <typename G> int ring_bytes(const AddNormArgs& a, int* stages) {
 int add_norm_device_error() { return read_clear_device_error(); }
 
 cudaError_t launch_add_norm_backward(const AddNormArgs& a, float* ws, cudaStream_t st) {
-  return an::by_geometry(a, [&](auto geo) {
-    using G = decltype(geo);
-    const long long groups = (a.rows + G::kRows - 1) / G::kRows;
-    int most = an::kMaxBlocks;
-    int stages = 0;
-    const int smem = an::ring_bytes<G>(a, &stages);
-    if (stages) most = most / 4 * an::kRingBlocks<G::kTPR>;
-    const int grid = static_cast<int>(groups < most ? groups : most);
-    const int parts = grid * G::kRows;
-    float* part_w = a.grad_w ? ws : nullptr;
-    float* part_post =
-        a.grad_w_post ? ws + (a.grad_w ? (size_t)parts * a.d : (size_t)0) : nullptr;
-    cudaError_t e = cudaSuccess;
-    if constexpr (G::kTPR > 32 && G::kTPR <= 512 && G::kV > 1) {
-      if (stages) {
-        const auto kernel = a.d == G::kCH * G::kV * G::kTPR
-                                ? an::add_norm_ring_backward<typename G::Full>
-                                : an::add_norm_ring_backward<G>;
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        kernel<<<grid, G::kTPR + 32, smem, st>>>(a, part_w, part_post, stages);
-      }
-    }
-    if (!stages) an::add_norm_rows_backward<G><<<grid, G::kThreads, 0, st>>>(a, part_w, part_post);
-    e = cudaPeekAtLastError();
-    if (e != cudaSuccess || !(part_w || part_post)) return e;
-    an::sum_partials<<<dim3(cdiv(a.d, 32), 2), 32 * an::kReduceWarps, 0, st>>>(
-        part_w, part_post, a.grad_w, a.grad_w_post, parts, a.d);
-    return cudaPeekAtLastError();
-  });
+  int parts = 0;
+  cudaError_t e = an::through_ring(a, ws, &parts, st);
+  if (e != cudaSuccess) return e;
+  if (!parts) {
+    e = an::by_geometry(a, [&](auto geo) {
+      using G = decltype(geo);
+      const long long groups = (a.rows + G::kRows - 1) / G::kRows;
+      const int grid = static_cast<int>(groups < an::kMaxBlocks ? groups : an::kMaxBlocks);
+      parts = grid * G::kRows;
+      float* part_post =
+          a.grad_w_post ? ws + (a.grad_w ? (size_t)parts * a.d : (size_t)0) : nullptr;
+      an::add_norm_rows_backward<G>
+          <<<grid, G::kThreads, 0, st>>>(a, a.grad_w ? ws : nullptr, part_post);
+      return cudaPeekAtLastError();
+    });
+  }
+  if (e != cudaSuccess || !(a.grad_w || a.grad_w_post)) return e;
+  const float* part_post = ws + (a.grad_w ? (size_t)parts * a.d : (size_t)0);
+  an::sum_partials<<<dim3(cdiv(a.d, 32), 2), 32 * an::kReduceWarps, 0, st>>>(
+      a.grad_w ? ws : nullptr, a.grad_w_post ? part_post : nullptr, a.grad_w, a.grad_w_post, parts,
+      a.d);
+  return cudaPeekAtLastError();
 }
 
 }  // namespace ret

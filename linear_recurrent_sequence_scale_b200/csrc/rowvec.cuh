@@ -164,13 +164,15 @@ template <typename T, int V, int CH, int TPR, bool FULL = false> struct RowPart 
   }
   // Zeros past d again.
   __device__ __forceinline__ void clear_rest(int lane, int nv) {
-    if (FULL || nv == CH * TPR) return;
+    if constexpr (!FULL) {
+      if (nv == CH * TPR) return;
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
-      if (c * TPR + lane >= nv) {
+      for (int c = 0; c < CH; ++c)
+        if (c * TPR + lane >= nv) {
 #pragma unroll
-        for (int k = 0; k < V; ++k) put(c * V + k, 0.0f);
-      }
+          for (int k = 0; k < V; ++k) put(c * V + k, 0.0f);
+        }
+    }
   }
   // v <- (v - [mean]) r, r = 1 / sqrt(mean square + eps); returns r.  sum(x)
   // adds x over the row's threads.  A row that does not exist gets r = 0.
