@@ -107,9 +107,15 @@ def version() -> str:
     return load_library().ret_version().decode()
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t) -> int:
@@ -462,13 +468,14 @@ def _pitches(shape, dtype, device, **operands):
 def _call(name, device, *args):
     """Runs a library call on the current stream of `device`, with that device
     current; raises on a status other than RET_OK."""
-    torch = _torch()
-    lib = load_library()
-    if device.index == torch.cuda.current_device():
-        s = getattr(lib, name)(*args, torch.cuda.current_stream(device).cuda_stream)
-    else:
-        with torch.cuda.device(device):
-            s = getattr(lib, name)(*args, torch.cuda.current_stream(device).cuda_stream)
+    cuda = _torch().cuda
+    index = device.index
+    if index != cuda.current_device():
+        with cuda.device(device):
+            return _call(name, device, *args)
+    # the raw handle: a Stream object costs as much as the library call itself
+    stream = _torch()._C._cuda_getCurrentRawStream(index)
+    s = getattr(_lib or load_library(), name)(*args, stream)
     if s != RET_OK:
         _raise(name, s)
 

@@ -16,6 +16,8 @@
 // decay drops all that was before it.  The state itself is carried as z = h
 // (LOG) or z = -h (LOGIT), which makes a step two fused operations without a
 // negation: z + q z + x, and z + q z + q x.
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "rowvec.cuh"
@@ -351,18 +353,27 @@ template <int OPERANDS, int TOK> struct Ring {
   static constexpr int kBytes = kStages * kStage;  // two blocks per SM
 };
 
-// The items of a block, one after another.
-struct Walk {
+// The items of a block, one after another: dealt in the order in time, or,
+// where the block keeps whole pieces, each piece from its first turn to its
+// last.
+template <bool WHOLE> struct Walk {
   int turn;  // place in the order that state flows: 0 has no predecessor
   int rest;  // batch row and piece of its channels in one
   __device__ __forceinline__ Walk(const Plan& p)
-      : turn(blockIdx.x / p.pieces), rest(blockIdx.x % p.pieces) {}
+      : turn(WHOLE ? 0 : blockIdx.x / p.pieces),
+        rest(WHOLE ? blockIdx.x : blockIdx.x % p.pieces) {}
   __device__ __forceinline__ void next(const Plan& p) {
-    turn += p.skip_turns;
-    rest += p.skip_rest;
-    if (rest >= p.pieces) rest -= p.pieces, ++turn;
+    if constexpr (WHOLE) {
+      if (++turn == p.tiles) turn = 0, rest += gridDim.x;
+    } else {
+      turn += p.skip_turns;
+      rest += p.skip_rest;
+      if (rest >= p.pieces) rest -= p.pieces, ++turn;
+    }
   }
-  __device__ __forceinline__ bool ends(const Plan& p) const { return turn >= p.tiles; }
+  __device__ __forceinline__ bool ends(const Plan& p) const {
+    return WHOLE ? rest >= p.pieces : turn >= p.tiles;
+  }
 };
 
 // What the scout hands to the computing warps: what enters the item of round
@@ -392,31 +403,45 @@ template <int STAGES, int n> __device__ __forceinline__ void open_desk(Desk<STAG
 }
 
 // The scout's rounds.  first(rest): what enters a turn 0 item.
-template <int STAGES, int n, typename First>
+template <bool WHOLE, int STAGES, int n, typename First>
 __device__ __forceinline__ void scout(Desk<STAGES, n>& desk, const Plan& p, int site,
                                       First first) {
   const int lane = threadIdx.x % 32;
-  Walk w(p);
-  for (int k = 0; !w.ends(p); ++k, w.next(p)) {
-    const Vec<n> z = w.turn > 0 ? look_back<n>(p, p.words(w, n, lane), p.pitch(n), w.turn, site)
-                                : first(w.rest);
-    // the slot's previous contents (round k - 2) have been read
-    if (k >= 2) sm100::mbar_wait(&desk.free[k % 2], (k / 2 - 1) % 2, site + 2);
-    desk.enter[k % 2][lane] = z;
+  Walk<WHOLE> w(p);
+  if constexpr (WHOLE) {  // the last computing warp hands each end on by itself
+    if (!w.ends(p)) desk.enter[0][lane] = first(w.rest);
     __syncwarp();
-    if (lane == 0) sm100::mbar_arrive(&desk.full[k % 2]);
+    if (lane == 0) sm100::mbar_arrive(&desk.full[0]);
+  } else {
+    for (int k = 0; !w.ends(p); ++k, w.next(p)) {
+      const Vec<n> z = w.turn > 0
+                           ? look_back<n>(p, p.words(w, n, lane), p.pitch(n), w.turn, site)
+                           : first(w.rest);
+      // the slot's previous contents (round k - 2) have been read
+      if (k >= 2) sm100::mbar_wait(&desk.free[k % 2], (k / 2 - 1) % 2, site + 2);
+      desk.enter[k % 2][lane] = z;
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(&desk.full[k % 2]);
+    }
   }
 }
 
-// By the computing warps: what enters the item of round k.
-template <int STAGES, int n>
+// By the computing warps: what enters the item of round k.  Where the block
+// keeps whole pieces it was put there in round k - 1, on the far side of this
+// round's barrier (only round 0 has it from the scout).
+template <bool WHOLE, int STAGES, int n>
 __device__ __forceinline__ Vec<n> entering(Desk<STAGES, n>& desk, int k, int site) {
-  sm100::mbar_wait(&desk.full[k % 2], (k / 2) % 2, site + 4);
   const int lane = threadIdx.x % 32;
-  const Vec<n> z = desk.enter[k % 2][lane];
-  __syncwarp();
-  if (lane == 0) sm100::mbar_arrive(&desk.free[k % 2]);
-  return z;
+  if constexpr (WHOLE) {
+    if (k == 0) sm100::mbar_wait(&desk.full[0], 0, site + 4);
+    return desk.enter[k % 2][lane];
+  } else {
+    sm100::mbar_wait(&desk.full[k % 2], (k / 2) % 2, site + 4);
+    const Vec<n> z = desk.enter[k % 2][lane];
+    __syncwarp();
+    if (lane == 0) sm100::mbar_arrive(&desk.free[k % 2]);
+    return z;
+  }
 }
 
 // An operand as TMA sees it: [D] x the pitch that is smaller x the larger one.
@@ -438,13 +463,13 @@ __device__ __forceinline__ void tma_store(const Mapped& m, const void* src, int 
 // place of some of them, those are stored and the slot is filled again.  Rows
 // and channels past the end read as zeros and are not written.  tile(turn):
 // place in time.  out[i]: the operand whose place result i has taken.
-template <int IN, int OUT, int TOK, int STAGES, int n, typename Tile>
+template <bool WHOLE, int IN, int OUT, int TOK, int STAGES, int n, typename Tile>
 __device__ __forceinline__ void mover(Desk<STAGES, n>& desk, char* ring, const Plan& p,
                                       const Mapped* in, const Mapped* out, const int (&place)[OUT],
                                       int site, Tile tile) {
   using R = Ring<IN, TOK>;
   constexpr int C = 32 * n;
-  Walk ahead(p), w(p);
+  Walk<WHOLE> ahead(p), w(p);
   int loads[STAGES];
 #pragma unroll
   for (int s = 0; s < STAGES; ++s) loads[s] = 0;
@@ -506,7 +531,7 @@ template <int FORM, int n> __device__ __forceinline__ void mask(Vec<n>& q, bool 
 // 16, TMA moves the items: the loads cost the computing warps nothing, and y
 // leaves from the place of f without an address or a bound being computed.
 // Otherwise the computing warps copy, and store y themselves.
-template <typename T, int FORM, bool GATE, int W>
+template <typename T, int FORM, bool GATE, int W, bool WHOLE>
 __global__ void __launch_bounds__(kBlockOf<W>, 2)
 scan_items(const ScanArgs a, const Plan p, const __grid_constant__ Maps<GATE ? 4 : 3, W> maps) {
   constexpr int IN = GATE ? 3 : 2;  // f, x, gate
@@ -520,25 +545,27 @@ scan_items(const ScanArgs a, const Plan p, const __grid_constant__ Maps<GATE ? 4
   __shared__ V agg_q[2][kWarps][32], agg_z[2][kWarps][32];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
+  const auto first = [&](int rest) {  // z before a sequence
+    const int b = rest / p.blocks, d = (rest - b * p.blocks) * C + lane * n;
+    return turn<FORM>(
+        get_state<n>(a.state_in && rest < p.pieces ? a.state_in + (size_t)b * a.D + d : nullptr,
+                     a.D - d));
+  };
   open_desk(desk);
   if (warp == kWarps) {
-    scout(desk, p, kSiteForward, [&](int rest) {
-      const int b = rest / p.blocks, d = (rest - b * p.blocks) * C + lane * n;
-      return turn<FORM>(
-          get_state<n>(a.state_in ? a.state_in + (size_t)b * a.D + d : nullptr, a.D - d));
-    });
+    scout<WHOLE>(desk, p, kSiteForward, first);
     return;
   }
   if constexpr (kTma) {
     if (warp > kWarps) {
       if (lane == 0)
-        mover<IN, 1, kTok>(desk, ring, p, maps.m, maps.m + IN, {0}, kSiteForward,
+        mover<WHOLE, IN, 1, kTok>(desk, ring, p, maps.m, maps.m + IN, {0}, kSiteForward,
                            [](int turn) { return turn; });
       return;
     }
   }
 
-  Walk ahead(p), w(p);
+  Walk<WHOLE> ahead(p), w(p);
   const auto load = [&](int slot) {
     if (!ahead.ends(p)) {
       const int b = ahead.rest / p.blocks, d = (ahead.rest - b * p.blocks) * C;
@@ -596,13 +623,18 @@ scan_items(const ScanArgs a, const Plan p, const __grid_constant__ Maps<GATE ? 4
       Qb = chain(Qb, agg_q[k % 2][v][lane]);
     }
     const bool publish = warp == kWarps - 1 && w.turn + 1 < p.tiles;
-    if (publish) {
+    if (warp == kWarps - 1) {
       Z = fold(Zb, Q, Z);
       Q = chain(Qb, Q);
-      st_words(p.span + 2 * p.words(w, n, lane), Q, Z);
+      if (publish && !WHOLE) st_words(p.span + 2 * p.words(w, n, lane), Q, Z);
     }
-    V z = entering(desk, k, kSiteForward);
-    if (publish) st_words(p.end + p.words(w, n, lane), fold(z, Q, Z));
+    V z = entering<WHOLE>(desk, k, kSiteForward);
+    if (warp == kWarps - 1) {
+      if constexpr (WHOLE)
+        desk.enter[(k + 1) % 2][lane] = publish ? fold(z, Q, Z) : first(w.rest + gridDim.x);
+      else if (publish)
+        st_words(p.end + p.words(w, n, lane), fold(z, Q, Z));
+    }
     z = fold(z, Qb, Zb);
 
     // 3. the same tokens from the z that enters them
@@ -648,7 +680,7 @@ scan_items(const ScanArgs a, const Plan p, const __grid_constant__ Maps<GATE ? 4
 // sequence, of one chunk each: the state that enters the chunk comes from the
 // forward call, h is recomputed in float32 inside it, and the flow is looked
 // for in the items after it as the forward does in those before.
-template <typename T, int FORM, bool GATE, int W>
+template <typename T, int FORM, bool GATE, int W, bool WHOLE>
 __global__ void __launch_bounds__(kBlockOf<W>, 2)
 scan_items_backward(const ScanArgs a, const Plan p,
                     const __grid_constant__ Maps<GATE ? 7 : 5, W> maps) {
@@ -663,12 +695,14 @@ scan_items_backward(const ScanArgs a, const Plan p,
   __shared__ V agg_q[2][kWarps][32], agg_z[2][kWarps][32], agg_e[2][kWarps][32];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
+  const auto first = [&](int rest) {  // the flow behind a sequence
+    const int b = rest / p.blocks, d = (rest - b * p.blocks) * C + lane * n;
+    return get_state<n>(
+        a.d_state_out && rest < p.pieces ? a.d_state_out + (size_t)b * a.D + d : nullptr, a.D - d);
+  };
   open_desk(desk);
   if (warp == kWarps) {
-    scout(desk, p, kSiteBackward, [&](int rest) {
-      const int b = rest / p.blocks, d = (rest - b * p.blocks) * C + lane * n;
-      return get_state<n>(a.d_state_out ? a.d_state_out + (size_t)b * a.D + d : nullptr, a.D - d);
-    });
+    scout<WHOLE>(desk, p, kSiteBackward, first);
     return;
   }
   if constexpr (kTma) {
@@ -676,15 +710,15 @@ scan_items_backward(const ScanArgs a, const Plan p,
       const auto tile = [&](int turn) { return p.tiles - 1 - turn; };
       if (lane == 0) {
         if constexpr (GATE)
-          mover<IN, 3, kTok>(desk, ring, p, maps.m, maps.m + IN, {0, 1, 3}, kSiteBackward, tile);
+          mover<WHOLE, IN, 3, kTok>(desk, ring, p, maps.m, maps.m + IN, {0, 1, 3}, kSiteBackward, tile);
         else
-          mover<IN, 2, kTok>(desk, ring, p, maps.m, maps.m + IN, {0, 1}, kSiteBackward, tile);
+          mover<WHOLE, IN, 2, kTok>(desk, ring, p, maps.m, maps.m + IN, {0, 1}, kSiteBackward, tile);
       }
       return;
     }
   }
 
-  Walk ahead(p), w(p);
+  Walk<WHOLE> ahead(p), w(p);
   const auto load = [&](int slot) {
     if (!ahead.ends(p)) {
       const int b = ahead.rest / p.blocks, d = (ahead.rest - b * p.blocks) * C;
@@ -760,10 +794,10 @@ scan_items_backward(const ScanArgs a, const Plan p,
       Qb = chain(Qb, agg_q[k % 2][v][lane]);
     }
     const bool publish = warp == 0 && w.turn + 1 < p.tiles;
-    if (publish) {
+    if (warp == 0) {
       E = fold(Eb, Q, E);
       Q = chain(Qb, Q);
-      st_words(p.span + 2 * p.words(w, n, lane), Q, E);
+      if (publish && !WHOLE) st_words(p.span + 2 * p.words(w, n, lane), Q, E);
     }
     // z forwards from the state that enters the chunk
     z = turn<FORM>(z);
@@ -782,8 +816,13 @@ scan_items_backward(const ScanArgs a, const Plan p,
     }
 
     // 3. the gradients, backwards
-    V flow = entering(desk, k, kSiteBackward);
-    if (publish) st_words(p.end + p.words(w, n, lane), fold(flow, Q, E));
+    V flow = entering<WHOLE>(desk, k, kSiteBackward);
+    if (warp == 0) {
+      if constexpr (WHOLE)
+        desk.enter[(k + 1) % 2][lane] = publish ? fold(flow, Q, E) : first(w.rest + gridDim.x);
+      else if (publish)
+        st_words(p.end + p.words(w, n, lane), fold(flow, Q, E));
+    }
     flow = fold(flow, Qb, Eb);
 #pragma unroll
     for (int j = S - 1; j >= 0; --j) {
@@ -917,35 +956,66 @@ cudaError_t map_operand(Mapped* m, const Operand& o, const ScanArgs& a, int tok)
              : make_tmap_rows(&m->map, o.p, es, a.D, a.N, a.B, token, batch, box, tok, 1);
 }
 
-// Blocks of a kernel that fit on the current device at once.
+// Whether blocks keep whole pieces, of `most` that run at once: then neither
+// the workspace nor a cooperative launch is needed, but a block's rounds follow
+// one another, and are as many as the fullest block's.  Worth it up to ten
+// rounds (4 us less for 256 x 256 in float32), and where few are wasted (8 x
+// 2048 x 2048 gated: 16 rounds instead of 13.8, 64 us either way); 2 x 8192 x
+// 4096 takes 111 us in whole pieces, 93 dealt.
+constexpr int kFewRounds = 10;
+bool keeps_whole(const Plan& p, int most) {
+  const int64_t rounds = (int64_t)p.tiles * ((p.pieces + most - 1) / most);
+  return rounds <= kFewRounds || rounds - 3 <= p.items / most;
+}
+
+// Sizes whose calls keep whole pieces on any device: they need no workspace.
+bool always_whole(int pieces, int N) {
+  return cdiv(N, kTokBackward) <= kFewRounds && pieces <= 128;
+}
+
+// What a kernel needs from the runtime, asked once per device: the permission
+// for its shared memory, and how many of its blocks run at once.
+constexpr int kMaxDevices = 64;
+using Known = std::atomic<int>[kMaxDevices];  // blocks, 0 until asked
+
 template <typename Kernel>
-cudaError_t resident(Kernel kernel, int threads, int smem, int* blocks) {
+cudaError_t resident(Kernel dealt, Kernel whole, int threads, int smem, Known& known,
+                     int* blocks) {
   int dev = 0, per_sm = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < kMaxDevices && (*blocks = known[dev].load()) > 0) return cudaSuccess;
+  for (Kernel k : {dealt, whole})
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess)
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, dealt, threads, smem);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   *blocks = per_sm * sms;
-  return e != cudaSuccess || *blocks > 0 ? e : cudaErrorInvalidConfiguration;
+  if (e != cudaSuccess) return e;
+  if (*blocks < 1) return cudaErrorInvalidConfiguration;
+  if (dev < kMaxDevices) known[dev].store(*blocks);
+  return cudaSuccess;
 }
 
 // tok: tokens of an item; ops: the kernel's operands in the order of its maps.
 template <int W, int OPERANDS>
-cudaError_t run(void (*kernel)(ScanArgs, Plan, Maps<OPERANDS, W>), const ScanArgs& a, int tok,
-                int smem, const Operand* const (&ops)[OPERANDS], cudaStream_t st) {
+cudaError_t run(void (*dealt)(ScanArgs, Plan, Maps<OPERANDS, W>),
+                void (*whole)(ScanArgs, Plan, Maps<OPERANDS, W>), const ScanArgs& a, int tok,
+                int smem, const Operand* const (&ops)[OPERANDS], Known& known, cudaStream_t st) {
   int most = 0;
-  cudaError_t e = resident(kernel, kBlockOf<W>, smem, &most);
+  cudaError_t e = resident(dealt, whole, kBlockOf<W>, smem, known, &most);
   if (e != cudaSuccess) return e;
   Plan p = plan(a, tok);
-  const int grid = p.items < most ? p.items : most;
+  const bool keep = always_whole(p.pieces, a.N) || keeps_whole(p, most);
+  const auto kernel = keep ? whole : dealt;
+  const int units = keep ? p.pieces : p.items, grid = units < most ? units : most;
   p.skip_turns = grid / p.pieces, p.skip_rest = grid % p.pieces;
   Maps<OPERANDS, W> maps;
   if constexpr (W == 16)
     for (int i = 0; i < OPERANDS; ++i)
       if ((e = map_operand(&maps.m[i], *ops[i], a, tok)) != cudaSuccess) return e;
-  if (p.tiles == 1) {  // nothing to wait for
+  if (keep) {  // nothing to wait for
     kernel<<<grid, kBlockOf<W>, smem, st>>>(a, p, maps);
     return cudaPeekAtLastError();
   }
@@ -964,26 +1034,28 @@ cudaError_t run(void (*kernel)(ScanArgs, Plan, Maps<OPERANDS, W>), const ScanArg
 
 template <typename T, int F, bool G, int W>
 cudaError_t forward(const ScanArgs& a, cudaStream_t st) {
+  static Known known;
   constexpr int smem = Ring<G ? 3 : 2, kTokForward>::kBytes;
   if constexpr (G) {
     const Operand* const ops[] = {&a.f, &a.x, &a.gate, &a.y};
-    return run<W>(scan_items<T, F, G, W>, a, kTokForward, smem, ops, st);
+    return run<W>(scan_items<T, F, G, W, false>, scan_items<T, F, G, W, true>, a, kTokForward, smem, ops, known, st);
   } else {
     const Operand* const ops[] = {&a.f, &a.x, &a.y};
-    return run<W>(scan_items<T, F, G, W>, a, kTokForward, smem, ops, st);
+    return run<W>(scan_items<T, F, G, W, false>, scan_items<T, F, G, W, true>, a, kTokForward, smem, ops, known, st);
   }
 }
 
 template <typename T, int F, bool G, int W>
 cudaError_t backward(const ScanArgs& a, cudaStream_t st) {
+  static Known known;
   constexpr int smem = Ring<G ? 4 : 3, kTokBackward>::kBytes;
   if constexpr (G) {
     const Operand* const ops[] = {&a.f,      &a.x,      &a.d_y,      &a.gate,
                                   &a.grad_f, &a.grad_x, &a.grad_gate};
-    return run<W>(scan_items_backward<T, F, G, W>, a, kTokBackward, smem, ops, st);
+    return run<W>(scan_items_backward<T, F, G, W, false>, scan_items_backward<T, F, G, W, true>, a, kTokBackward, smem, ops, known, st);
   } else {
     const Operand* const ops[] = {&a.f, &a.x, &a.d_y, &a.grad_f, &a.grad_x};
-    return run<W>(scan_items_backward<T, F, G, W>, a, kTokBackward, smem, ops, st);
+    return run<W>(scan_items_backward<T, F, G, W, false>, scan_items_backward<T, F, G, W, true>, a, kTokBackward, smem, ops, known, st);
   }
 }
 
@@ -991,11 +1063,11 @@ cudaError_t backward(const ScanArgs& a, cudaStream_t st) {
 
 int scan_device_error() { return read_clear_device_error(); }
 
-// For either direction: the backward's items are the shorter ones.  A
-// sequence of one item needs none.
+// For either direction: the backward's items are the shorter ones.
 size_t scan_workspace_bytes(int B, int N, int D, int dtype) {
   const int tiles = cdiv(N, scan::kTokBackward);
-  return tiles > 1 ? 12 * scan::words(B, D, dtype, tiles) : 0;
+  if (tiles == 1 || scan::always_whole(B * cdiv(D, scan::channels_per_piece(dtype)), N)) return 0;
+  return 12 * scan::words(B, D, dtype, tiles);
 }
 
 cudaError_t launch_scan(const ScanArgs& a, cudaStream_t st) {

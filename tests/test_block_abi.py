@@ -66,11 +66,17 @@ def test_scan_refusals(lib):
     assert bad(dense=True, N=1 << 30, D=1 << 12) == ret.RET_EUNSUPPORTED
     assert bad(px=(1 << 60, 64)) == ret.RET_EUNSUPPORTED
     assert bad(px=(64, 1 << 60)) == ret.RET_EUNSUPPORTED
-    need = lib.ret_scan_workspace(2, 300, 64, 1)
-    if need:
-        assert bad(ws=None) == ret.RET_EWORKSPACE
-        assert bad(wsb=need - 1) == ret.RET_EWORKSPACE
-        assert bad(ws=off(A[3], 8)) == ret.RET_EINVAL
+    # short sequences of few channels need no workspace, long ones 12 bytes for each
+    # 64 tokens of a channel (rounded up to pieces of 128 bytes of a row)
+    assert lib.ret_scan_workspace(2, 300, 64, 1) == 0
+    need = lib.ret_scan_workspace(2, 900, 70, 1)
+    assert need == 12 * 15 * 2 * 128
+    assert lib.ret_scan_workspace(2, 900, 70, 0) == 12 * 15 * 2 * 96
+    long = dict(N=900, D=70, dense=True)
+    assert bad(ws=None, **long) == ret.RET_EWORKSPACE
+    assert bad(wsb=need - 1, **long) == ret.RET_EWORKSPACE
+    assert bad(ws=off(A[3], 8), **long) == ret.RET_EINVAL
+    assert bad(y=A[3], **long) == ret.RET_EINVAL             # the workspace over y
     assert lib.ret_scan_workspace(0, 300, 64, 1) == 0
     assert lib.ret_scan_workspace(2, 0, 64, 1) == 0
     # no tokens and no state wanted: nothing to do
