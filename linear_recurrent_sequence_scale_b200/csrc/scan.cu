@@ -341,16 +341,33 @@ template <int FORM, int n> __device__ __forceinline__ Vec<n> turn(Vec<n> h) {
   return vec(r);
 }
 
-constexpr int kTokForward = 128, kTokBackward = RET_SCAN_CHUNK;
-static_assert(kTokForward % RET_SCAN_CHUNK == 0, "chunk states are kept at warp boundaries");
-static_assert((kTokForward / kWarps) * (RET_SCAN_CHUNK / (kTokForward / kWarps)) == RET_SCAN_CHUNK,
-              "a chunk is a whole number of warps' tokens");
+// Shape of the work: one block per SM with long items, or two with half as many
+// tokens each.  Long items make a warp's work large against its share of the
+// folds, barriers and look-back (65536 x 4096 in bf16: 346 us with two blocks
+// of 128 tokens, 299 with one of 256; 8 x 2048 x 2048 gated backward: 102 us
+// with two of 64, 95 with one of 128).  With the gate's pass the forward has
+// work enough as it is, and two blocks hide each other's waits (8 x 2048 x 2048
+// gated: 60 us, 64 with one); likewise where the computing warps copy their
+// items (3 x 1501 x 1001 backward in float32: 45 us, 50 with one).
+template <bool GATE, int W> constexpr int kForwardBlocks = W == 16 && !GATE ? 1 : 2;
+template <int W> constexpr int kBackwardBlocks = W == 16 ? 1 : 2;
+template <bool GATE, int W> constexpr int kTokForward = 256 / kForwardBlocks<GATE, W>;
+template <int W> constexpr int kTokBackward = 128 / kBackwardBlocks<W>;
+constexpr int kTokLeast = 64;  // of any item
 
-template <int OPERANDS, int TOK> struct Ring {
+template <int OPERANDS, int TOK, int BLOCKS> struct Ring {
   static constexpr int kOperand = TOK * kPiece;
   static constexpr int kStage = OPERANDS * kOperand;
-  static constexpr int kStages = kStage <= 32 * 1024 ? 3 : 2;
-  static constexpr int kBytes = kStages * kStage;  // two blocks per SM
+  static constexpr int kFit = 200 * 1024 / BLOCKS / kStage;
+  // Two blocks stop at three: where rows are not 16-byte aligned the L1 beside
+  // the ring serves the lines that two pieces share (43 us with four stages,
+  // 35 with three, for the float32 backward above).
+  static constexpr int kMost = BLOCKS == 1 ? 4 : 3;
+  static constexpr int kStages = kFit < kMost ? kFit : kMost;
+  static constexpr int kBytes = kStages * kStage;
+  static_assert(kStages >= 2 && TOK >= kTokLeast && TOK % RET_SCAN_CHUNK == 0 &&
+                    RET_SCAN_CHUNK % (TOK / kWarps) == 0,
+                "chunk states are kept and read where a warp's tokens begin");
 };
 
 // The items of a block, one after another: dealt in the order in time, or,
@@ -463,11 +480,10 @@ __device__ __forceinline__ void tma_store(const Mapped& m, const void* src, int 
 // place of some of them, those are stored and the slot is filled again.  Rows
 // and channels past the end read as zeros and are not written.  tile(turn):
 // place in time.  out[i]: the operand whose place result i has taken.
-template <bool WHOLE, int IN, int OUT, int TOK, int STAGES, int n, typename Tile>
+template <bool WHOLE, typename R, int IN, int OUT, int TOK, int STAGES, int n, typename Tile>
 __device__ __forceinline__ void mover(Desk<STAGES, n>& desk, char* ring, const Plan& p,
                                       const Mapped* in, const Mapped* out, const int (&place)[OUT],
                                       int site, Tile tile) {
-  using R = Ring<IN, TOK>;
   constexpr int C = 32 * n;
   Walk<WHOLE> ahead(p), w(p);
   int loads[STAGES];
@@ -532,11 +548,11 @@ template <int FORM, int n> __device__ __forceinline__ void mask(Vec<n>& q, bool 
 // leaves from the place of f without an address or a bound being computed.
 // Otherwise the computing warps copy, and store y themselves.
 template <typename T, int FORM, bool GATE, int W, bool WHOLE>
-__global__ void __launch_bounds__(kBlockOf<W>, 2)
+__global__ void __launch_bounds__(kBlockOf<W>, (kForwardBlocks<GATE, W>))
 scan_items(const ScanArgs a, const Plan p, const __grid_constant__ Maps<GATE ? 4 : 3, W> maps) {
   constexpr int IN = GATE ? 3 : 2;  // f, x, gate
-  using R = Ring<IN, kTokForward>;
-  constexpr int n = kLane<T>, kTok = kTokForward, S = kTok / kWarps, C = 32 * n;
+  using R = Ring<IN, kTokForward<GATE, W>, kForwardBlocks<GATE, W>>;
+  constexpr int n = kLane<T>, kTok = kTokForward<GATE, W>, S = kTok / kWarps, C = 32 * n;
   constexpr int ST = R::kStages, kX = R::kOperand, kGate = 2 * R::kOperand;
   constexpr bool kTma = W == 16;
   using V = Vec<n>;
@@ -559,7 +575,7 @@ scan_items(const ScanArgs a, const Plan p, const __grid_constant__ Maps<GATE ? 4
   if constexpr (kTma) {
     if (warp > kWarps) {
       if (lane == 0)
-        mover<WHOLE, IN, 1, kTok>(desk, ring, p, maps.m, maps.m + IN, {0}, kSiteForward,
+        mover<WHOLE, R, IN, 1, kTok>(desk, ring, p, maps.m, maps.m + IN, {0}, kSiteForward,
                            [](int turn) { return turn; });
       return;
     }
@@ -677,16 +693,16 @@ scan_items(const ScanArgs a, const Plan p, const __grid_constant__ Maps<GATE ? 4
 // What flows to the token before, E_t = a_t G_t, obeys the same kind of
 // recurrence in reversed time: a span turns the flow e behind it into
 // E + e + Q e with the same Q.  So the items are taken from the end of the
-// sequence, of one chunk each: the state that enters the chunk comes from the
+// sequence: the state that enters a chunk comes from the
 // forward call, h is recomputed in float32 inside it, and the flow is looked
 // for in the items after it as the forward does in those before.
 template <typename T, int FORM, bool GATE, int W, bool WHOLE>
-__global__ void __launch_bounds__(kBlockOf<W>, 2)
+__global__ void __launch_bounds__(kBlockOf<W>, kBackwardBlocks<W>)
 scan_items_backward(const ScanArgs a, const Plan p,
                     const __grid_constant__ Maps<GATE ? 7 : 5, W> maps) {
   constexpr int IN = GATE ? 4 : 3;  // f, x, d_y, gate; grad_f, grad_x and grad_gate in their place
-  using R = Ring<IN, kTokBackward>;
-  constexpr int n = kLane<T>, kTok = kTokBackward, S = kTok / kWarps, C = 32 * n;
+  using R = Ring<IN, kTokBackward<W>, kBackwardBlocks<W>>;
+  constexpr int n = kLane<T>, kTok = kTokBackward<W>, S = kTok / kWarps, C = 32 * n;
   constexpr int ST = R::kStages, kX = R::kOperand, kDy = 2 * R::kOperand, kGate = 3 * R::kOperand;
   constexpr bool kTma = W == 16;
   using V = Vec<n>;
@@ -710,9 +726,9 @@ scan_items_backward(const ScanArgs a, const Plan p,
       const auto tile = [&](int turn) { return p.tiles - 1 - turn; };
       if (lane == 0) {
         if constexpr (GATE)
-          mover<WHOLE, IN, 3, kTok>(desk, ring, p, maps.m, maps.m + IN, {0, 1, 3}, kSiteBackward, tile);
+          mover<WHOLE, R, IN, 3, kTok>(desk, ring, p, maps.m, maps.m + IN, {0, 1, 3}, kSiteBackward, tile);
         else
-          mover<WHOLE, IN, 2, kTok>(desk, ring, p, maps.m, maps.m + IN, {0, 1}, kSiteBackward, tile);
+          mover<WHOLE, R, IN, 2, kTok>(desk, ring, p, maps.m, maps.m + IN, {0, 1}, kSiteBackward, tile);
       }
       return;
     }
@@ -744,8 +760,12 @@ scan_items_backward(const ScanArgs a, const Plan p,
   for (int k = 0, slot = 0, phase = 0; !w.ends(p); ++k, w.next(p)) {
     const int b = w.rest / p.blocks, d = (w.rest - b * p.blocks) * C + lane * n, left = a.D - d;
     const int tile = p.tiles - 1 - w.turn, t0 = tile * kTok + warp * S, mine = min(S, a.N - t0);
-    // what enters the chunk: read here, needed after 1
-    V z = get_state<n>(a.chunk_states + ((size_t)b * p.tiles + tile) * a.D + d, left);
+    // what enters the chunk of this warp's tokens: read here, needed after 1
+    const int chunk = t0 / RET_SCAN_CHUNK, head = warp - t0 % RET_SCAN_CHUNK / S;
+    V z = get_state<n>(
+        mine > 0 ? a.chunk_states + ((size_t)b * cdiv(a.N, RET_SCAN_CHUNK) + chunk) * a.D + d
+                 : nullptr,
+        left);
     if constexpr (kTma) {
       sm100::mbar_wait(&desk.loaded[slot], phase, kSiteBackward + 8);
     } else {
@@ -801,7 +821,7 @@ scan_items_backward(const ScanArgs a, const Plan p,
     }
     // z forwards from the state that enters the chunk
     z = turn<FORM>(z);
-    for (int v = 0; v < warp; ++v) z = fold(z, agg_q[k % 2][v][lane], agg_z[k % 2][v][lane]);
+    for (int v = head; v < warp; ++v) z = fold(z, agg_q[k % 2][v][lane], agg_z[k % 2][v][lane]);
     V before[S];
 #pragma unroll
     for (int j = 0; j < S; ++j) {
@@ -970,7 +990,7 @@ bool keeps_whole(const Plan& p, int most) {
 
 // Sizes whose calls keep whole pieces on any device: they need no workspace.
 bool always_whole(int pieces, int N) {
-  return cdiv(N, kTokBackward) <= kFewRounds && pieces <= 128;
+  return cdiv(N, kTokLeast) <= kFewRounds && pieces <= 128;
 }
 
 // What a kernel needs from the runtime, asked once per device: the permission
@@ -1035,27 +1055,27 @@ cudaError_t run(void (*dealt)(ScanArgs, Plan, Maps<OPERANDS, W>),
 template <typename T, int F, bool G, int W>
 cudaError_t forward(const ScanArgs& a, cudaStream_t st) {
   static Known known;
-  constexpr int smem = Ring<G ? 3 : 2, kTokForward>::kBytes;
+  constexpr int smem = Ring<G ? 3 : 2, kTokForward<G, W>, kForwardBlocks<G, W>>::kBytes;
   if constexpr (G) {
     const Operand* const ops[] = {&a.f, &a.x, &a.gate, &a.y};
-    return run<W>(scan_items<T, F, G, W, false>, scan_items<T, F, G, W, true>, a, kTokForward, smem, ops, known, st);
+    return run<W>(scan_items<T, F, G, W, false>, scan_items<T, F, G, W, true>, a, kTokForward<G, W>, smem, ops, known, st);
   } else {
     const Operand* const ops[] = {&a.f, &a.x, &a.y};
-    return run<W>(scan_items<T, F, G, W, false>, scan_items<T, F, G, W, true>, a, kTokForward, smem, ops, known, st);
+    return run<W>(scan_items<T, F, G, W, false>, scan_items<T, F, G, W, true>, a, kTokForward<G, W>, smem, ops, known, st);
   }
 }
 
 template <typename T, int F, bool G, int W>
 cudaError_t backward(const ScanArgs& a, cudaStream_t st) {
   static Known known;
-  constexpr int smem = Ring<G ? 4 : 3, kTokBackward>::kBytes;
+  constexpr int smem = Ring<G ? 4 : 3, kTokBackward<W>, kBackwardBlocks<W>>::kBytes;
   if constexpr (G) {
     const Operand* const ops[] = {&a.f,      &a.x,      &a.d_y,      &a.gate,
                                   &a.grad_f, &a.grad_x, &a.grad_gate};
-    return run<W>(scan_items_backward<T, F, G, W, false>, scan_items_backward<T, F, G, W, true>, a, kTokBackward, smem, ops, known, st);
+    return run<W>(scan_items_backward<T, F, G, W, false>, scan_items_backward<T, F, G, W, true>, a, kTokBackward<W>, smem, ops, known, st);
   } else {
     const Operand* const ops[] = {&a.f, &a.x, &a.d_y, &a.grad_f, &a.grad_x};
-    return run<W>(scan_items_backward<T, F, G, W, false>, scan_items_backward<T, F, G, W, true>, a, kTokBackward, smem, ops, known, st);
+    return run<W>(scan_items_backward<T, F, G, W, false>, scan_items_backward<T, F, G, W, true>, a, kTokBackward<W>, smem, ops, known, st);
   }
 }
 
@@ -1063,9 +1083,9 @@ cudaError_t backward(const ScanArgs& a, cudaStream_t st) {
 
 int scan_device_error() { return read_clear_device_error(); }
 
-// For either direction: the backward's items are the shorter ones.
+// For either direction and any alignment: as many items as the shortest make.
 size_t scan_workspace_bytes(int B, int N, int D, int dtype) {
-  const int tiles = cdiv(N, scan::kTokBackward);
+  const int tiles = cdiv(N, scan::kTokLeast);
   if (tiles == 1 || scan::always_whole(B * cdiv(D, scan::channels_per_piece(dtype)), N)) return 0;
   return 12 * scan::words(B, D, dtype, tiles);
 }
