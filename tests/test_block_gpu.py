@@ -106,6 +106,10 @@ SCAN = [
     case("f32", "log", 1, 4100, 64, state=True),
     case("bf16", "log", 1, 9000, 64, gate=True, state=True),
     case("f32", "logit", 5, 700, 1001, gate=True, state=True, fused=True),
+    # too long for whole pieces: items dealt over the blocks, at every alignment
+    case("bf16", "logit", 2, 3001, 72, state=True, fused=True),
+    case("bf16", "logit", 2, 3001, 65, gate=True), case("bf16", "log", 1, 2817, 130, state=True),
+    case("f32", "logit", 1, 2819, 31, state=True), case("f32", "log", 3, 2690, 36, gate=True),
 ]
 ids = lambda c: "-".join(str(v) for v in c.values())  # noqa: E731
 
@@ -259,13 +263,14 @@ def test_scan_leaves_neighbours_alone(torch, ret):
     assert (buf[mask] == 5).all()
 
 
-def test_scan_streams_and_graphs(torch, ret):
-    """Calls on two streams at once, and a captured pair of calls replayed on new
-    inputs."""
-    c = case("bf16", "logit", 2, 1000, 128, gate=True, state=True)
+@pytest.mark.parametrize("N,D", [(1000, 128), (5000, 128), (5000, 131)])
+def test_scan_streams_and_graphs(torch, ret, N, D):
+    """Calls on several streams at once, and a captured pair of calls replayed on new
+    inputs: in whole pieces, and dealt over the blocks of a cooperative launch."""
+    c = case("bf16", "logit", 2, N, D, gate=True, state=True)
     _, x, f, g, s0 = scan_inputs(torch, c, seed=8)
     want = ret.scan(x, f, gate=g, state_in=s0, return_state=True, return_chunk_states=True)
-    d_y = Draws(torch, "bf16", 9).normal(2, 1000, 128)
+    d_y = Draws(torch, "bf16", 9).normal(2, N, D)
     back = ret.scan_backward(x, f, want[2], d_y, gate=g)
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in range(3)]
@@ -293,6 +298,45 @@ def test_scan_streams_and_graphs(torch, ret):
             assert all(torch.equal(a, b) for a, b in zip(grads, back))
         else:
             assert torch.equal(y, ret.scan(x2, f, gate=g, state_in=s0))
+
+
+def test_scan_graphs_share_a_workspace(torch, ret):
+    """Two captured calls and an eager one use the same workspace in turn."""
+    c = case("f32", "log", 1, 4000, 96, state=True)
+    _, x, f, _, s0 = scan_inputs(torch, c, seed=10)
+    ws = torch.empty(ret.scan_workspace_bytes(1, 4000, 96, x.dtype), device="cuda",
+                     dtype=torch.uint8)
+    assert ws.numel() > 0
+    want, half = ret.scan(x, f, form="log", state_in=s0), ret.scan(0.5 * x, f, form="log")
+    graphs, outs = [], []
+    xs = [x.clone(), 0.5 * x]
+    for xi, s in zip(xs, (s0, None)):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(ret.scan(xi, f, form="log", state_in=s, workspace=ws))
+    for _ in range(3):
+        graphs[0].replay()
+        graphs[1].replay()
+        eager = ret.scan(x, f, form="log", state_in=s0, workspace=ws)
+        graphs[0].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want) and torch.equal(outs[1], half) and torch.equal(eager, want)
+
+
+def test_scan_offsets_past_32_bits(torch, ret):
+    """Batch rows more than 2^32 bytes apart, read and written."""
+    N, D, far = 300, 64, (1 << 31) + 64
+    d = Draws(torch, "bf16", 11)
+    room = [torch.empty(far + N * D, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    x, y = (r.as_strided((2, N, D), (far, D, 1)) for r in room)
+    x.copy_(d.normal(2, N, D))
+    f = forget(d, "logit", 2, N, D, False)
+    assert torch.equal(ret.scan(x, f, out=y), ret.scan(x.contiguous(), f))
+    _, cs = ret.scan(x, f, return_chunk_states=True)
+    d_y = d.normal(2, N, D)
+    got = ret.scan_backward(x, f, cs, d_y, grad_f=y)
+    want = ret.scan_backward(x.contiguous(), f, cs, d_y)
+    assert all(torch.equal(a, b) for a, b in zip(got, want) if a is not None)
 
 
 # --- norm and gate ----------------------------------------------------------------
@@ -402,6 +446,24 @@ def test_norm_gate_in_place(torch, ret):
                       out=y.view(2, 21, 3, 96))
 
 
+def test_norm_gate_offsets_past_32_bits(torch, ret):
+    """More than 2^31 elements; the last tokens of the last head are checked."""
+    B, H, N, dv = 2, 3, 699_200, 512
+    g0 = torch.Generator(device="cuda").manual_seed(1)
+    y = torch.randn(B, H, N, dv, device="cuda", dtype=torch.bfloat16, generator=g0)
+    assert y.numel() > 1 << 31
+    gate = torch.randn(B, N, H, dv, device="cuda", dtype=torch.bfloat16, generator=g0)
+    o = ret.norm_gate(y, gate, token_major=True)
+    tail = ret.norm_gate(y[-1:, :, -5:].contiguous(), gate[-1:, -5:].contiguous(),
+                         token_major=True)
+    assert torch.equal(o[-1:, -5:], tail)
+    del o
+    gy, gg = ret.norm_gate_backward(y, gate, gate, token_major=True)
+    ty, tg = ret.norm_gate_backward(y[-1:, :, -5:].contiguous(), gate[-1:, -5:].contiguous(),
+                                    gate[-1:, -5:].contiguous(), token_major=True)
+    assert torch.equal(gy[-1:, :, -5:], ty) and torch.equal(gg[-1:, -5:], tg)
+
+
 # --- residual and norms -------------------------------------------------------------
 
 ADD_NORM = [
@@ -420,6 +482,13 @@ ADD_NORM = [
     ("bf16", 2, 16383, None, "rms", True, True, True),
     ("bf16", 2500, 33, None, "rms", True, True, True),
     ("f32", 1300, 260, "layer", "rms", True, False, True),
+    ("bf16", 900, 512, "layer", "layer", True, True, True),
+    ("bf16", 1900, 1024, "rms", "layer", True, True, True),
+    ("f32", 500, 1024, "layer", "layer", True, True, True),
+    ("f32", 450, 4096, "rms", "layer", True, True, True),
+    ("bf16", 460, 4096, "layer", "rms", True, True, True),
+    ("bf16", 300, 8192, "rms", "rms", True, True, True),
+    ("bf16", 301, 6000, None, "layer", True, True, True),
 ]
 ALPHA, BETA = 1.5, 0.7
 
@@ -533,6 +602,25 @@ def test_add_norm_in_place_and_empty(torch, ret):
     assert ret.add_norm(none, none, w)[1].shape == (0, 1000)
     got = ret.add_norm_backward(none, none, w, none, w_post=wp)
     assert not got[2].any() and not got[3].any()
+
+
+def test_add_norm_offsets_past_32_bits(torch, ret):
+    """More than 2^31 elements; the last rows are checked."""
+    rows, dim = 1_050_000, 2048
+    g0 = torch.Generator(device="cuda").manual_seed(2)
+    x, r = (torch.randn(rows, dim, device="cuda", dtype=torch.bfloat16, generator=g0)
+            for _ in range(2))
+    assert x.numel() > 1 << 31
+    w = torch.rand(dim, device="cuda", generator=g0)
+    kw = dict(w_post=w, post_norm="rms", norm="layer", alpha=ALPHA, beta=BETA)
+    got = ret.add_norm(x, r, w, **kw)
+    want = ret.add_norm(x[-7:].clone(), r[-7:].clone(), w, **kw)
+    assert all(torch.equal(a[-7:], b) for a, b in zip(got, want))
+    del got
+    got = ret.add_norm_backward(x, r, w, r, x, **kw)
+    want = ret.add_norm_backward(x[-7:].clone(), r[-7:].clone(), w, r[-7:].clone(),
+                                 x[-7:].clone(), **kw)
+    assert all(torch.equal(a[-7:], b) for a, b in zip(got[:2], want[:2]))
 
 
 # --- a run of them together ---------------------------------------------------------
