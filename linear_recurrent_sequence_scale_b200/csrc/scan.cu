@@ -238,56 +238,42 @@ __device__ __forceinline__ Vec<n> look_back(const Plan& p, size_t at, size_t pit
 }
 
 // ---- moving an item into shared memory ------------------------------------------
-template <int W> __device__ __forceinline__ void cp_async(uint32_t dst, const char* src, bool ok) {
-  const int n = ok ? W : 0;  // 0: writes zeros, reads nothing
-  if constexpr (W == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-                 : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n)
-                 : "memory");
+// 16 bytes, of which the first n are read and the others become zeros.
+__device__ __forceinline__ void cp_async(uint32_t dst, const char* src, int n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// TOK rows of kPiece bytes: rows past `rows` and bytes past `bytes` become
-// zeros.  W: bytes per access; 2 (rows aligned to a bf16 only) has no
-// asynchronous form and goes through registers.
-template <int W, int TOK>
+// Rows that are not 16-byte aligned are copied as the 16-byte granules that
+// cover them, nine for a piece, and read from where they begin in the first:
+// a granule's bytes before the row are read along (they lie in the row's own
+// 16 bytes of memory), those behind the piece or the row's end are not.
+// Copied 4 bytes at a time, 8 x 2048 x 2046 in bf16 took 122 us gated and 222
+// backward, and with a bf16's alignment (2047), through registers, 427 and
+// 557; in granules 102 and 185, 118 and 181.
+constexpr int kGranules = kPiece / 16 + 1;
+template <int W> constexpr int kRow = W == 16 ? kPiece : 16 * kGranules;  // in shared memory
+
+// TOK rows of kPiece bytes: rows past `rows` and bytes past `bytes` become zeros.
+template <int TOK>
 __device__ __forceinline__ void copy_item(char* dst, const char* src, long long pitch, int rows,
                                           int bytes) {
-  if constexpr (W >= 4) {
-    constexpr int kPer = kPiece / W, kStep = kCompute / kPer;
-    const int col = (threadIdx.x % kPer) * W, r0 = threadIdx.x / kPer;
-    const uint32_t d = sm100::smem_u32(dst) + r0 * kPiece + col;
-    if (rows >= TOK && bytes >= kPiece) {
-      const char* s = src + r0 * pitch + col;
+  const uint32_t to = sm100::smem_u32(dst);
+  const int width = min(bytes, kPiece);
 #pragma unroll
-      for (int i = 0; i < TOK / kStep; ++i, s += kStep * pitch)
-        cp_async<W>(d + i * kStep * kPiece, s, true);
-    } else {
-#pragma unroll
-      for (int i = 0; i < TOK / kStep; ++i) {
-        const int r = i * kStep + r0;
-        const bool ok = r < rows && col < bytes;
-        cp_async<W>(d + i * kStep * kPiece, ok ? src + r * pitch + col : src, ok);
-      }
-    }
-  } else {
-    const int col = (threadIdx.x % 32) * 4;
-#pragma unroll 8
-    for (int i = 0; i < TOK / kWarps; ++i) {
-      const int r = i * kWarps + threadIdx.x / 32;
-      uint32_t v = 0;
-      if (r < rows) {
-        const unsigned short* q = reinterpret_cast<const unsigned short*>(src + r * pitch + col);
-        if (col < bytes) v = q[0];
-        if (col + 2 < bytes) v |= (uint32_t)q[1] << 16;
-      }
-      *reinterpret_cast<uint32_t*>(dst + r * kPiece + col) = v;
-    }
+  for (int k = 0; k < (TOK * kGranules + kCompute - 1) / kCompute; ++k) {
+    const int i = k * kCompute + threadIdx.x;
+    if ((k + 1) * kCompute > TOK * kGranules && i >= TOK * kGranules) break;
+    const int r = i / kGranules, g = i - r * kGranules;
+    const uintptr_t start = reinterpret_cast<uintptr_t>(src) + r * pitch;
+    const uintptr_t granule = (start & ~(uintptr_t)15) + 16 * g;
+    const int n = r < rows ? max(0, min(16, (int)(start + width - granule))) : 0;
+    cp_async(to + i * 16, reinterpret_cast<const char*>(n > 0 ? granule : start & ~(uintptr_t)15),
+             n);
   }
 }
 
@@ -298,6 +284,12 @@ __device__ __forceinline__ void compute_sync() {
 
 // The channels of one lane: 4 bytes of a row.
 template <typename T> constexpr int kLane = 4 / sizeof(T);
+// One operand's rows of a warp's tokens in shared memory: where the first one's
+// granules begin, and the low bits of its address and pitch in memory.
+struct Rows {
+  char* p;
+  uint32_t low, pitch;
+};
 template <typename T> __device__ __forceinline__ Vec<kLane<T>> get(const char* row) {
   float r[kLane<T>];
   load_pack<T, kLane<T>>(reinterpret_cast<const T*>(row) + (threadIdx.x % 32) * kLane<T>, r);
@@ -308,6 +300,23 @@ template <typename T, int n> __device__ __forceinline__ void set(char* row, cons
 #pragma unroll
   for (int i = 0; i < n; ++i) v[i] = x[i];
   store_pack<T, n>(reinterpret_cast<T*>(row) + (threadIdx.x % 32) * n, v);
+}
+template <typename T, int W>
+__device__ __forceinline__ Vec<kLane<T>> get(const Rows& rows, int j) {
+  if constexpr (W == 16) {
+    return get<T>(rows.p + j * kRow<W>);
+  } else {
+    const char* row = rows.p + j * kRow<W> + ((rows.low + j * rows.pitch) & 15);
+    if constexpr (W >= 4) {
+      return get<T>(row);
+    } else {
+      const T* q = reinterpret_cast<const T*>(row) + (threadIdx.x % 32) * kLane<T>;
+      float r[kLane<T>];
+#pragma unroll
+      for (int i = 0; i < kLane<T>; ++i) r[i] = Elem<T>::ld(q + i);
+      return vec(r);
+    }
+  }
 }
 // `left`: channels of the piece that exist from this lane's first one on.
 template <typename T, bool PAIR, int n>
@@ -347,23 +356,20 @@ template <int FORM, int n> __device__ __forceinline__ Vec<n> turn(Vec<n> h) {
 // of 128 tokens, 299 with one of 256; 8 x 2048 x 2048 gated backward: 102 us
 // with two of 64, 95 with one of 128).  With the gate's pass the forward has
 // work enough as it is, and two blocks hide each other's waits (8 x 2048 x 2048
-// gated: 60 us, 64 with one); likewise where the computing warps copy their
-// items (3 x 1501 x 1001 backward in float32: 45 us, 50 with one).
-template <bool GATE, int W> constexpr int kForwardBlocks = W == 16 && !GATE ? 1 : 2;
-template <int W> constexpr int kBackwardBlocks = W == 16 ? 1 : 2;
+// gated: 60 us, 64 with one).
+template <bool GATE, int W> constexpr int kForwardBlocks = W == 16 && GATE ? 2 : 1;
+constexpr int kBackwardBlocks = 1;
 template <bool GATE, int W> constexpr int kTokForward = 256 / kForwardBlocks<GATE, W>;
-template <int W> constexpr int kTokBackward = 128 / kBackwardBlocks<W>;
+constexpr int kTokBackward = 128 / kBackwardBlocks;
 constexpr int kTokLeast = 64;  // of any item
 
-template <int OPERANDS, int TOK, int BLOCKS> struct Ring {
-  static constexpr int kOperand = TOK * kPiece;
+// SUMS: span sums that the warps exchange beside the ring, 4 KB each.
+template <int OPERANDS, int SUMS, int TOK, int BLOCKS, int W> struct Ring {
+  static constexpr int kOperand = TOK * kRow<W>;
   static constexpr int kStage = OPERANDS * kOperand;
-  static constexpr int kFit = 200 * 1024 / BLOCKS / kStage;
-  // Two blocks stop at three: where rows are not 16-byte aligned the L1 beside
-  // the ring serves the lines that two pieces share (43 us with four stages,
-  // 35 with three, for the float32 backward above).
-  static constexpr int kMost = BLOCKS == 1 ? 4 : 3;
-  static constexpr int kStages = kFit < kMost ? kFit : kMost;
+  static constexpr int kRoom = 227 * 1024 / BLOCKS - 1024 * (4 * SUMS + 2 * BLOCKS - 1);
+  static constexpr int kFit = kRoom / kStage;
+  static constexpr int kStages = kFit < 4 ? kFit : 4;
   static constexpr int kBytes = kStages * kStage;
   static_assert(kStages >= 2 && TOK >= kTokLeast && TOK % RET_SCAN_CHUNK == 0 &&
                     RET_SCAN_CHUNK % (TOK / kWarps) == 0,
@@ -551,7 +557,7 @@ template <typename T, int FORM, bool GATE, int W, bool WHOLE>
 __global__ void __launch_bounds__(kBlockOf<W>, (kForwardBlocks<GATE, W>))
 scan_items(const ScanArgs a, const Plan p, const __grid_constant__ Maps<GATE ? 4 : 3, W> maps) {
   constexpr int IN = GATE ? 3 : 2;  // f, x, gate
-  using R = Ring<IN, kTokForward<GATE, W>, kForwardBlocks<GATE, W>>;
+  using R = Ring<IN, 2, kTokForward<GATE, W>, kForwardBlocks<GATE, W>, W>;
   constexpr int n = kLane<T>, kTok = kTokForward<GATE, W>, S = kTok / kWarps, C = 32 * n;
   constexpr int ST = R::kStages, kX = R::kOperand, kGate = 2 * R::kOperand;
   constexpr bool kTma = W == 16;
@@ -587,12 +593,12 @@ scan_items(const ScanArgs a, const Plan p, const __grid_constant__ Maps<GATE ? 4
       const int b = ahead.rest / p.blocks, d = (ahead.rest - b * p.blocks) * C;
       const int t = ahead.turn * kTok, rows = a.N - t, bytes = (a.D - d) * (int)sizeof(T);
       char* s = ring + slot * R::kStage;
-      copy_item<W, kTok>(s, (const char*)at<const T>(a.f, b, t, d), a.f.token * sizeof(T), rows,
+      copy_item<kTok>(s, (const char*)at<const T>(a.f, b, t, d), a.f.token * sizeof(T), rows,
                          bytes);
-      copy_item<W, kTok>(s + kX, (const char*)at<const T>(a.x, b, t, d), a.x.token * sizeof(T),
+      copy_item<kTok>(s + kX, (const char*)at<const T>(a.x, b, t, d), a.x.token * sizeof(T),
                          rows, bytes);
       if constexpr (GATE)
-        copy_item<W, kTok>(s + kGate, (const char*)at<const T>(a.gate, b, t, d),
+        copy_item<kTok>(s + kGate, (const char*)at<const T>(a.gate, b, t, d),
                            a.gate.token * sizeof(T), rows, bytes);
       ahead.next(p);
     }
@@ -611,16 +617,24 @@ scan_items(const ScanArgs a, const Plan p, const __grid_constant__ Maps<GATE ? 4
       compute_sync();  // the item is here, and the previous one's slot is free
       load(slot == 0 ? ST - 1 : slot - 1);
     }
-    char* f = ring + slot * R::kStage + warp * S * kPiece;
+    const auto rows = [&](const Operand& o, int place) {
+      Rows r = {ring + slot * R::kStage + place + warp * S * kRow<W>, 0, 0};
+      if constexpr (!kTma) {
+        r.low = (uint32_t) reinterpret_cast<uintptr_t>(at<const T>(o, b, t0, d - lane * n));
+        r.pitch = (uint32_t)o.token * sizeof(T);
+      }
+      return r;
+    };
+    const Rows f = rows(a.f, 0), x = rows(a.x, kX);
 
     // 1. this warp's tokens from zero
     V q[S], Q = all<n>(0.0f), Z = Q;
     const auto from_zero = [&](auto whole) {
 #pragma unroll
       for (int j = 0; j < S; ++j) {
-        q[j] = less_one<FORM>(get<T>(f + j * kPiece));
+        q[j] = less_one<FORM>(get<T, W>(f, j));
         if (!decltype(whole)::value) mask<FORM>(q[j], j < mine);
-        Z = advance<FORM>(Z, q[j], get<T>(f + kX + j * kPiece));
+        Z = advance<FORM>(Z, q[j], get<T, W>(x, j));
         Q = chain(Q, q[j]);
       }
     };
@@ -661,11 +675,11 @@ scan_items(const ScanArgs a, const Plan p, const __grid_constant__ Maps<GATE ? 4
     T* y = kTma ? nullptr : at<T>(a.y, b, t0, d);
 #pragma unroll
     for (int j = 0; j < S; ++j) {
-      z = advance<FORM>(z, q[j], get<T>(f + kX + j * kPiece));
+      z = advance<FORM>(z, q[j], get<T, W>(x, j));
       V out = turn<FORM>(z);
-      if constexpr (GATE) out = mul(out, swish(get<T>(f + kGate + j * kPiece)));
+      if constexpr (GATE) out = mul(out, swish(get<T, W>(rows(a.gate, kGate), j)));
       if constexpr (kTma) {
-        set<T>(f + j * kPiece, out);
+        set<T>(f.p + j * kRow<W>, out);
       } else {
         if (j < mine) put<T, (W >= 4)>(y, out, left);
         y += a.y.token;
@@ -697,12 +711,12 @@ scan_items(const ScanArgs a, const Plan p, const __grid_constant__ Maps<GATE ? 4
 // forward call, h is recomputed in float32 inside it, and the flow is looked
 // for in the items after it as the forward does in those before.
 template <typename T, int FORM, bool GATE, int W, bool WHOLE>
-__global__ void __launch_bounds__(kBlockOf<W>, kBackwardBlocks<W>)
+__global__ void __launch_bounds__(kBlockOf<W>, kBackwardBlocks)
 scan_items_backward(const ScanArgs a, const Plan p,
                     const __grid_constant__ Maps<GATE ? 7 : 5, W> maps) {
   constexpr int IN = GATE ? 4 : 3;  // f, x, d_y, gate; grad_f, grad_x and grad_gate in their place
-  using R = Ring<IN, kTokBackward<W>, kBackwardBlocks<W>>;
-  constexpr int n = kLane<T>, kTok = kTokBackward<W>, S = kTok / kWarps, C = 32 * n;
+  using R = Ring<IN, 3, kTokBackward, kBackwardBlocks, W>;
+  constexpr int n = kLane<T>, kTok = kTokBackward, S = kTok / kWarps, C = 32 * n;
   constexpr int ST = R::kStages, kX = R::kOperand, kDy = 2 * R::kOperand, kGate = 3 * R::kOperand;
   constexpr bool kTma = W == 16;
   using V = Vec<n>;
@@ -741,14 +755,14 @@ scan_items_backward(const ScanArgs a, const Plan p,
       const int t = (p.tiles - 1 - ahead.turn) * kTok;
       const int rows = a.N - t, bytes = (a.D - d) * (int)sizeof(T);
       char* s = ring + slot * R::kStage;
-      copy_item<W, kTok>(s, (const char*)at<const T>(a.f, b, t, d), a.f.token * sizeof(T), rows,
+      copy_item<kTok>(s, (const char*)at<const T>(a.f, b, t, d), a.f.token * sizeof(T), rows,
                          bytes);
-      copy_item<W, kTok>(s + kX, (const char*)at<const T>(a.x, b, t, d), a.x.token * sizeof(T),
+      copy_item<kTok>(s + kX, (const char*)at<const T>(a.x, b, t, d), a.x.token * sizeof(T),
                          rows, bytes);
-      copy_item<W, kTok>(s + kDy, (const char*)at<const T>(a.d_y, b, t, d),
+      copy_item<kTok>(s + kDy, (const char*)at<const T>(a.d_y, b, t, d),
                          a.d_y.token * sizeof(T), rows, bytes);
       if constexpr (GATE)
-        copy_item<W, kTok>(s + kGate, (const char*)at<const T>(a.gate, b, t, d),
+        copy_item<kTok>(s + kGate, (const char*)at<const T>(a.gate, b, t, d),
                            a.gate.token * sizeof(T), rows, bytes);
       ahead.next(p);
     }
@@ -773,21 +787,31 @@ scan_items_backward(const ScanArgs a, const Plan p,
       compute_sync();
       load(slot == 0 ? ST - 1 : slot - 1);
     }
-    char* f = ring + slot * R::kStage + warp * S * kPiece;
+    const auto rows = [&](const Operand& o, int place) {
+      Rows r = {ring + slot * R::kStage + place + warp * S * kRow<W>, 0, 0};
+      if constexpr (!kTma) {
+        r.low = (uint32_t) reinterpret_cast<uintptr_t>(at<const T>(o, b, t0, d - lane * n));
+        r.pitch = (uint32_t)o.token * sizeof(T);
+      }
+      return r;
+    };
+    const Rows f = rows(a.f, 0), x = rows(a.x, kX), dy = rows(a.d_y, kDy);
+    Rows g = {};
+    if constexpr (GATE) g = rows(a.gate, kGate);
 
     // 1. this warp's tokens: forwards from a zero state, backwards from a zero flow
     V q[S], dh[S], slope[GATE ? S : 1], Q = all<n>(0.0f), Z = Q, E = Q;
     const auto from_zero = [&](auto whole) {
 #pragma unroll
       for (int j = 0; j < S; ++j) {
-        q[j] = less_one<FORM>(get<T>(f + j * kPiece));
+        q[j] = less_one<FORM>(get<T, W>(f, j));
         if (!decltype(whole)::value) mask<FORM>(q[j], j < mine);
-        Z = advance<FORM>(Z, q[j], get<T>(f + kX + j * kPiece));
+        Z = advance<FORM>(Z, q[j], get<T, W>(x, j));
         Q = chain(Q, q[j]);
-        dh[j] = get<T>(f + kDy + j * kPiece);
+        dh[j] = get<T, W>(dy, j);
         if constexpr (GATE) {
           V sw, sl;
-          swish_grad(get<T>(f + kGate + j * kPiece), &sw, &sl);
+          swish_grad(get<T, W>(g, j), &sw, &sl);
           slope[j] = turn<FORM>(mul(dh[j], sl));  // with the sign of z
           dh[j] = mul(dh[j], sw);
         }
@@ -826,10 +850,10 @@ scan_items_backward(const ScanArgs a, const Plan p,
 #pragma unroll
     for (int j = 0; j < S; ++j) {
       before[j] = z;
-      z = advance<FORM>(z, q[j], get<T>(f + kX + j * kPiece));
+      z = advance<FORM>(z, q[j], get<T, W>(x, j));
       if constexpr (GATE) {
         if constexpr (kTma)
-          set<T>(f + kGate + j * kPiece, mul(z, slope[j]));
+          set<T>(g.p + j * kRow<W>, mul(z, slope[j]));
         else if (j < mine)
           put<T, (W >= 4)>(at<T>(a.grad_gate, b, t0 + j, d), mul(z, slope[j]), left);
       }
@@ -851,11 +875,11 @@ scan_items_backward(const ScanArgs a, const Plan p,
       V dx = G, df = mul(before[j], flow);
       if (FORM == RET_SCAN_LOGIT) {
         dx = turn<FORM>(mul(q[j], G));
-        df = mul(mul(add(before[j], get<T>(f + kX + j * kPiece)), q[j]), flow);
+        df = mul(mul(add(before[j], get<T, W>(x, j)), q[j]), flow);
       }
       if constexpr (kTma) {
-        set<T>(f + kX + j * kPiece, dx);
-        set<T>(f + j * kPiece, df);
+        set<T>(x.p + j * kRow<W>, dx);
+        set<T>(f.p + j * kRow<W>, df);
       } else if (j < mine) {
         put<T, (W >= 4)>(at<T>(a.grad_x, b, t0 + j, d), dx, left);
         put<T, (W >= 4)>(at<T>(a.grad_f, b, t0 + j, d), df, left);
@@ -1055,7 +1079,7 @@ cudaError_t run(void (*dealt)(ScanArgs, Plan, Maps<OPERANDS, W>),
 template <typename T, int F, bool G, int W>
 cudaError_t forward(const ScanArgs& a, cudaStream_t st) {
   static Known known;
-  constexpr int smem = Ring<G ? 3 : 2, kTokForward<G, W>, kForwardBlocks<G, W>>::kBytes;
+  constexpr int smem = Ring<G ? 3 : 2, 2, kTokForward<G, W>, kForwardBlocks<G, W>, W>::kBytes;
   if constexpr (G) {
     const Operand* const ops[] = {&a.f, &a.x, &a.gate, &a.y};
     return run<W>(scan_items<T, F, G, W, false>, scan_items<T, F, G, W, true>, a, kTokForward<G, W>, smem, ops, known, st);
@@ -1068,14 +1092,14 @@ cudaError_t forward(const ScanArgs& a, cudaStream_t st) {
 template <typename T, int F, bool G, int W>
 cudaError_t backward(const ScanArgs& a, cudaStream_t st) {
   static Known known;
-  constexpr int smem = Ring<G ? 4 : 3, kTokBackward<W>, kBackwardBlocks<W>>::kBytes;
+  constexpr int smem = Ring<G ? 4 : 3, 3, kTokBackward, kBackwardBlocks, W>::kBytes;
   if constexpr (G) {
     const Operand* const ops[] = {&a.f,      &a.x,      &a.d_y,      &a.gate,
                                   &a.grad_f, &a.grad_x, &a.grad_gate};
-    return run<W>(scan_items_backward<T, F, G, W, false>, scan_items_backward<T, F, G, W, true>, a, kTokBackward<W>, smem, ops, known, st);
+    return run<W>(scan_items_backward<T, F, G, W, false>, scan_items_backward<T, F, G, W, true>, a, kTokBackward, smem, ops, known, st);
   } else {
     const Operand* const ops[] = {&a.f, &a.x, &a.d_y, &a.grad_f, &a.grad_x};
-    return run<W>(scan_items_backward<T, F, G, W, false>, scan_items_backward<T, F, G, W, true>, a, kTokBackward<W>, smem, ops, known, st);
+    return run<W>(scan_items_backward<T, F, G, W, false>, scan_items_backward<T, F, G, W, true>, a, kTokBackward, smem, ops, known, st);
   }
 }
 
