@@ -242,12 +242,26 @@ add_norm_rows_backward(AddNormArgs a, float* part_w, float* part_post) {
 // joining them (Chan, Golub and LeVeque's pairwise variance); and the weights
 // wait in shared memory.  65536 x 4096 in bf16, both norms and both weights:
 // 1027 us with loads in registers and five exchanges, 670 through rings of
-// two blocks per SM with 16 elements per thread, ANB_US with three groups of
+// two blocks per SM with 16 elements per thread, 600 with three groups of
 // 128 threads.
 constexpr int kSiteRing = 811;
 constexpr int kMaxStages = 4;
+// The same serves rows that are not 16-byte aligned: they come as the granules
+// that cover them (the bytes before a row lie in its own first 16 bytes of
+// memory; none behind it is read), and threads take single elements.  16384 x
+// 4095 in bf16: 824 us with single elements from HBM, 399 so.
+constexpr int kGranuleStages = 2;
 constexpr int kRingWarps = 12;  // three on each scheduler: 168 registers a thread
 constexpr int kRingBytes = 225 * 1024;  // beside 1 KB of barriers and sums
+
+// Bytes of the ring for a row of `bytes`.
+__host__ __device__ constexpr int ring_row(int bytes, bool whole) {
+  return whole ? bytes : (bytes + 14 + 15) / 16 * 16;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, uintptr_t src, int n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
 
 __device__ __forceinline__ Vec<2> warp_sum(Vec<2> x) {
 #pragma unroll
@@ -382,16 +396,24 @@ template <typename G> struct Block {
   }
   // v <- v (.) w
   static __device__ __forceinline__ void scale(Row<G>& v, const float* w, int lane, int nv) {
+    if constexpr (G::kV == 1) {
 #pragma unroll
-    for (int c = 0; c < G::kCH; ++c) {
-      const int i = c * G::kTPR + lane;
-      if (G::kFull || i < nv) {
+      for (int i = 0; i < Row<G>::P; ++i) {
+        const int c0 = 2 * i * G::kTPR + lane, c1 = c0 + G::kTPR;
+        v.p[i] = mul(v.p[i], two(c0 < nv ? w[c0] : 0.0f, c1 < nv ? w[c1] : 0.0f));
+      }
+    } else {
 #pragma unroll
-        for (int j = 0; j < G::kV; j += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(w + i * G::kV + j);
-          const int k = (c * G::kV + j) / 2;
-          v.p[k] = mul(v.p[k], two(f.x, f.y));
-          v.p[k + 1] = mul(v.p[k + 1], two(f.z, f.w));
+      for (int c = 0; c < G::kCH; ++c) {
+        const int i = c * G::kTPR + lane;
+        if (G::kFull || i < nv) {
+#pragma unroll
+          for (int j = 0; j < G::kV; j += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(w + i * G::kV + j);
+            const int k = (c * G::kV + j) / 2;
+            v.p[k] = mul(v.p[k], two(f.x, f.y));
+            v.p[k + 1] = mul(v.p[k + 1], two(f.z, f.w));
+          }
         }
       }
     }
@@ -411,7 +433,9 @@ add_norm_ring_backward(AddNormArgs a, float* part_w, float* part_post, int group
   __shared__ uint64_t full[kMaxGroups][kMaxStages];
   const bool post = a.post_norm != RET_NORM_NONE, need_x = post || part_post;
   const bool layer = a.norm == RET_NORM_LAYER, layer_post = a.post_norm == RET_NORM_LAYER;
-  const uint32_t row = a.d * (uint32_t)sizeof(T);
+  // a row's place in the ring: its bytes, or the 16-byte granules that cover it
+  constexpr bool kWhole = G::kV > 1;
+  const uint32_t row = ring_row(a.d * (int)sizeof(T), kWhole);
   const uint32_t stage = row * (2 + (a.d_res_out ? 1 : 0) + (need_x ? 1 : 0));
   // behind the groups' rings, the weights
   float* w = reinterpret_cast<float*>(ring + groups * stages * stage);
@@ -431,9 +455,30 @@ add_norm_ring_backward(AddNormArgs a, float* part_w, float* part_post, int group
   R acc_w, acc_post;
 #pragma unroll
   for (int i = 0; i < R::P; ++i) acc_w.p[i] = acc_post.p[i] = all<2>(0.0f);
-  // by the group's first thread: row n into stage s
+  // Row n into stage s: by the group's first thread, as bulk copies; rows that
+  // are not 16-byte aligned by all of its threads, granule by granule.
   const auto fetch = [&](long long n, int s) {
-    if (n >= a.rows) return;
+    if constexpr (!kWhole) {
+      if (n < a.rows) {
+        const uint32_t to = sm100::smem_u32(ring + (group * stages + s) * stage);
+        const auto copy = [&](const void* p, uint32_t place) {
+          const uintptr_t start = reinterpret_cast<uintptr_t>(static_cast<const T*>(p) + n * a.d);
+          const uintptr_t end = start + a.d * sizeof(T);
+          for (uint32_t at = lane * 16; at < row; at += G::kTPR * 16) {
+            const uintptr_t granule = (start & ~(uintptr_t)15) + at;
+            if (granule < end)
+              cp_async16(to + place + at, granule, end - granule < 16 ? (int)(end - granule) : 16);
+          }
+        };
+        copy(a.res_out, 0);
+        copy(a.d_y, row);
+        if (a.d_res_out) copy(a.d_res_out, 2 * row);
+        if (need_x) copy(a.x, stage - row);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      return;
+    }
+    if (lane != 0 || n >= a.rows) return;
     char* to = ring + (group * stages + s) * stage;
     const auto load = [&](const void* p, uint32_t place) {
       sm100::bulk_load(to + place, static_cast<const T*>(p) + n * a.d, row, &full[group][s]);
@@ -445,25 +490,31 @@ add_norm_ring_backward(AddNormArgs a, float* part_w, float* part_post, int group
     if (need_x) load(a.x, stage - row);
   };
   {
-    if (lane == 0)
-      for (int s = 0; s < stages; ++s) fetch(first + group + s * step, s);
+    for (int s = 0; s < stages; ++s) fetch(first + group + s * step, s);
     const float inv_d = 1.0f / a.d;
     int s = 0, phase = 0;
     for (long long n = first + group; n < a.rows; n += step) {
-      sm100::mbar_wait(&full[group][s], phase, kSiteRing + 1);
+      if constexpr (kWhole) {
+        sm100::mbar_wait(&full[group][s], phase, kSiteRing + 1);
+      } else {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kGranuleStages - 1) : "memory");
+        B::sync(group);
+      }
       const char* here = ring + (group * stages + s) * stage;
-      const auto load = [&](R& part, uint32_t place) {
-        part.load(reinterpret_cast<const T*>(here + place), lane, nv);
-      };
       const long long at = n * a.d;
+      const auto load = [&](R& part, uint32_t place, const void* p) {
+        const uint32_t off =
+            kWhole ? 0 : (uint32_t) reinterpret_cast<uintptr_t>(static_cast<const T*>(p) + at) & 15;
+        part.load(reinterpret_cast<const T*>(here + place + off), lane, nv);
+      };
       R h, d;
       // both norms' moments
       float2 mine_x = make_float2(0.0f, 0.0f);
       if (post) {
-        load(d, stage - row);
+        load(d, stage - row, a.x);
         mine_x = B::own(d, layer_post, lane, nv);
       }
-      load(h, 0);
+      load(h, 0, a.res_out);
       const float2 mine_h = B::own(h, layer, lane, nv);
       const Vec<2> m2 = warp_sum(two(mine_h.y, mine_x.y));
       if (lane % 32 == 0)
@@ -479,12 +530,12 @@ add_norm_ring_backward(AddNormArgs a, float* part_w, float* part_post, int group
       if (B::W == 1) __syncwarp();  // read before the next row's are written
       // through the norm before the next block
       B::apply(h, mh, layer, lane, nv);
-      load(d, row);
+      load(d, row, a.d_y);
       if (part_w) acc_w.add_product(d, h);
       if (a.w) B::scale(d, w, lane, nv);
       B::back(d, h, mh.r, layer, inv_d, slots[group][0], group, lane, nv);
       if (a.d_res_out) {
-        load(h, 2 * row);
+        load(h, 2 * row, a.d_res_out);
 #pragma unroll
         for (int i = 0; i < R::P; ++i) d.p[i] = add(d.p[i], h.p[i]);
       }
@@ -495,9 +546,9 @@ add_norm_ring_backward(AddNormArgs a, float* part_w, float* part_post, int group
       }
       d.times(a.beta);
       // and through the one after the block
-      if (need_x) load(h, stage - row);
+      if (need_x) load(h, stage - row, a.x);
       B::sync(group);  // the stage has been read
-      if (lane == 0) fetch(n + stages * step, s);
+      fetch(n + stages * step, s);
       if (post) B::apply(h, mx, layer_post, lane, nv);
       if (part_post) acc_post.add_product(d, h);
       if (a.grad_x) {
@@ -508,13 +559,14 @@ add_norm_ring_backward(AddNormArgs a, float* part_w, float* part_post, int group
       if (++s == stages) s = 0, phase ^= 1;
     }
     // where some wait gave up, the copies still under way end before the block does
-    if (lane == 0 && sm100::failed())
+    if (kWhole && lane == 0 && sm100::failed())
       for (int i = 0; i < stages; ++i) {
         const long long mine = a.rows - first - group;  // rows of the group: ceil(mine / step)
         const long long rows = mine > 0 ? (mine + step - 1) / step : 0;
         if (rows > i) sm100::mbar_drain(&full[group][i], ((rows - 1 - i) / stages) % 2);
       }
   }
+  if constexpr (!kWhole) asm volatile("cp.async.wait_group 0;" ::: "memory");
   // the groups' sums, through the place of their rings, in the groups' order
   float* sums = reinterpret_cast<float*>(ring);
   for (int which = 0; which < 2; ++which) {
@@ -620,13 +672,15 @@ template <typename G> RingPlan ring_plan(const AddNormArgs& a) {
   RingPlan p;
   const int tensors = 2 + (a.d_res_out ? 1 : 0) +
                       (a.post_norm != RET_NORM_NONE || a.grad_w_post ? 1 : 0);
-  const int stage = tensors * a.d * (int)sizeof(typename G::type);
+  const int stage = tensors * ring_row(a.d * (int)sizeof(typename G::type), G::kV > 1);
+  // (an odd width leaves the second weight's row unaligned: only single elements read it)
   const int weights = a.d * 4 * ((a.w ? 1 : 0) + (a.w_post ? 1 : 0));
   const int fit = (kRingBytes - weights) / (2 * stage), most = kRingWarps / (G::kTPR / 32);
   p.groups = fit < most ? fit : most;
   if (p.groups < 1) return RingPlan();
   p.stages = (kRingBytes - weights) / (p.groups * stage);
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  const int most_stages = G::kV > 1 ? kMaxStages : kGranuleStages;
+  if (p.stages > most_stages) p.stages = most_stages;
   p.smem = p.groups * p.stages * stage + weights;
   return p;
 }
@@ -651,14 +705,28 @@ cudaError_t run_ring(const AddNormArgs& a, float* ws, int* parts, cudaStream_t s
   return cudaPeekAtLastError();
 }
 
-// Rows of at least 512 bytes that split into 16-byte pieces, if two of them
-// fit; *parts stays 0 where the ring does not serve.
+template <typename T>
+cudaError_t by_elements(const AddNormArgs& a, float* ws, int* parts, cudaStream_t st) {
+  if (a.d <= 256) return run_ring<Geo<T, 1, 8, 32>>(a, ws, parts, st);
+  if (a.d <= 512) return run_ring<Geo<T, 1, 16, 32>>(a, ws, parts, st);
+  if (a.d <= 1024) return run_ring<Geo<T, 1, 32, 32>>(a, ws, parts, st);
+  if (a.d <= 2048) return run_ring<Geo<T, 1, 32, 64>>(a, ws, parts, st);
+  if (a.d <= 4096) return run_ring<Geo<T, 1, 32, 128>>(a, ws, parts, st);
+  if (a.d <= 8192) return run_ring<Geo<T, 1, 32, 256>>(a, ws, parts, st);
+  return cudaSuccess;
+}
+
+// Rows of at least 512 bytes, if two of them fit; *parts stays 0 where the ring
+// does not serve.
 cudaError_t through_ring(const AddNormArgs& a, float* ws, int* parts, cudaStream_t st) {
   using bf16 = __nv_bfloat16;
   *parts = 0;
   const bool half = a.dtype == RET_BF16;
+  if (a.d * (half ? 2 : 4) < 512) return cudaSuccess;
+  if (!vectored(a)) return half ? by_elements<bf16>(a, ws, parts, st)
+                                : by_elements<float>(a, ws, parts, st);
   const int nv = a.d * (half ? 2 : 4) / 16;
-  if (!vectored(a) || nv < 32 || nv > 1024) return cudaSuccess;
+  if (nv > 1024) return cudaSuccess;
   if (half) {
     if (nv <= 64) return run_ring<Geo<bf16, 8, 2, 32>>(a, ws, parts, st);
     if (nv <= 128) return run_ring<Geo<bf16, 8, 4, 32>>(a, ws, parts, st);

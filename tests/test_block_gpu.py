@@ -489,6 +489,11 @@ ADD_NORM = [
     ("bf16", 460, 4096, "layer", "rms", True, True, True),
     ("bf16", 300, 8192, "rms", "rms", True, True, True),
     ("bf16", 301, 6000, None, "layer", True, True, True),
+    ("bf16", 500, 4095, "rms", "layer", True, True, True),
+    ("bf16", 301, 1001, "layer", "rms", True, False, True),
+    ("f32", 400, 8191, "rms", "rms", True, True, True),
+    ("bf16", 1300, 301, "layer", "layer", True, True, True),
+    ("f32", 333, 1025, None, "rms", False, True, True),
 ]
 ALPHA, BETA = 1.5, 0.7
 
@@ -585,21 +590,22 @@ def test_add_norm_backward(torch, ret, c, with_res_grad):
     assert all(torch.equal(a, b) for a, b in zip(got, twice) if a is not None)
 
 
-def test_add_norm_in_place_and_empty(torch, ret):
-    c = ("bf16", 37, 1000, "rms", "rms", True, True, True)
+@pytest.mark.parametrize("dim", [1000, 1001])
+def test_add_norm_in_place_and_empty(torch, ret, dim):
+    c = ("bf16", 3700, dim, "rms", "rms", True, True, True)
     d, x, r, w, wp = add_norm_inputs(torch, c, 23)
     kw = dict(w_post=wp, post_norm="rms", norm="rms", alpha=ALPHA, beta=BETA)
     want = ret.add_norm(x, r, w, **kw)
     r2, x2 = r.clone(), x.clone()
     got = ret.add_norm(x2, r2, w, res_out=r2, out=x2, **kw)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
-    d_y, d_r = d.normal(37, 1000), d.normal(37, 1000)
+    d_y, d_r = d.normal(3700, dim), d.normal(3700, dim)
     want = ret.add_norm_backward(x, r, w, d_y, d_r, **kw)
     dy2, dr2 = d_y.clone(), d_r.clone()
     got = ret.add_norm_backward(x, r, w, dy2, dr2, grad_x=dy2, grad_residual=dr2, **kw)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
-    none = torch.empty(0, 1000, device="cuda", dtype=torch.bfloat16)
-    assert ret.add_norm(none, none, w)[1].shape == (0, 1000)
+    none = torch.empty(0, dim, device="cuda", dtype=torch.bfloat16)
+    assert ret.add_norm(none, none, w)[1].shape == (0, dim)
     got = ret.add_norm_backward(none, none, w, none, w_post=wp)
     assert not got[2].any() and not got[3].any()
 
