@@ -22,6 +22,7 @@ RET_OK, RET_EINVAL, RET_EUNSUPPORTED, RET_ECUDA, RET_EWORKSPACE = 0, -1, -2, -3,
 SCAN_CHUNK = 64                                    # RET_SCAN_CHUNK
 SCAN_FORMS = {"logit": 0, "log": 1}                # ret_scan_form
 NORMS = {None: -1, "layer": 0, "rms": 1}           # ret_norm_kind
+ROW_NORMS = {"layer": 0, "rms": 1}
 
 # name -> (restype, argtypes) of every symbol include/retention.h declares
 _P, _I, _F, _S = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
@@ -430,36 +431,55 @@ def _code(names, name, what):
         raise ValueError(f"unknown {what} {name!r}; use one of {list(names)}") from None
 
 
+# The calls below serve single tokens as well, where the host's time counts:
+# checks pass on one comparison each and explain themselves only on failure.
+
 def _same(t, name, dtype, shape, device):
+    if t.dtype is dtype and t.device == device and t.shape == shape and t.is_cuda:
+        return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-def _pitches(shape, dtype, device, **operands):
-    """Pitches (elements) of the [..., D] operands, in order: a host array for
-    the library with one entry per leading axis of each, or None when all are
-    dense.  Channels must be adjacent; the library checks the rest."""
-    strided = False
-    for name, t in operands.items():
+def _dense(t, name, dtype, shape, device):
+    _same(t, name, dtype, shape, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _like(x):
+    """A new dense tensor of x's shape and type."""
+    return _torch().empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
+
+
+def _pitches(x, names, *operands):
+    """Pitches (elements) of x and the other [..., D] operands (None: absent), in
+    order: a host array for the library with one entry per leading axis of
+    each, or None when all are dense.  Channels must be adjacent; the library
+    checks the rest."""
+    shape, dtype, device = x.shape, x.dtype, x.device
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    dense = x.is_contiguous()
+    for t, name in zip(operands, names):
         if t is not None:
             _same(t, name, dtype, shape, device)
-            strided = strided or not t.is_contiguous()
-    if not strided:
+            dense = dense and t.is_contiguous()
+    if dense:
         return None
     lead = len(shape) - 1
     got = []
-    for name, t in operands.items():
+    for t, name in zip((x,) + operands, ("x",) + names):
         if t is None:
             got += [0] * lead
             continue
         st = t.stride()
-        if shape[-1] > 1 and st[-1] != 1:
+        if st[-1] != 1 and shape[-1] > 1:
             raise ValueError(f"{name}: channels must be adjacent, got strides {st}")
         got += st[:-1]
     return (_L * len(got))(*got)
@@ -468,14 +488,13 @@ def _pitches(shape, dtype, device, **operands):
 def _call(name, device, *args):
     """Runs a library call on the current stream of `device`, with that device
     current; raises on a status other than RET_OK."""
-    cuda = _torch().cuda
+    torch = _torch()
     index = device.index
-    if index != cuda.current_device():
-        with cuda.device(device):
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(device):
             return _call(name, device, *args)
     # the raw handle: a Stream object costs as much as the library call itself
-    stream = _torch()._C._cuda_getCurrentRawStream(index)
-    s = getattr(_lib or load_library(), name)(*args, stream)
+    s = getattr(_lib or load_library(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
     if s != RET_OK:
         _raise(name, s)
 
@@ -496,7 +515,7 @@ def _own_workspace(workspace, need, device):
 
 def _state(t, name, shape, device):
     if t is not None:
-        _check(t, name, dtype=_torch().float32, shape=shape, device=device)
+        _dense(t, name, _torch().float32, shape, device)
 
 
 def scan_workspace_bytes(B, N, D, dtype) -> int:
@@ -522,21 +541,20 @@ def scan(x, f, form="logit", gate=None, state_in=None, state_out=None, return_st
     torch = _torch()
     if x.dim() != 3:
         raise ValueError("x must be [B,N,D]")
-    shape, dev, dt = x.shape, x.device, x.dtype
+    dev = x.device
     code, kind = _dtype_code(x), _code(SCAN_FORMS, form, "form")
-    B, N, D = shape
+    B, N, D = x.shape
     _state(state_in, "state_in", (B, D), dev)
     if state_out is None and return_state:
-        state_out = torch.empty((B, D), dtype=torch.float32, device=dev)
+        state_out = x.new_empty((B, D), dtype=torch.float32)
     else:
         _state(state_out, "state_out", (B, D), dev)
     if chunk_states is None and return_chunk_states:
-        chunk_states = torch.empty((B, -(-N // SCAN_CHUNK), D), dtype=torch.float32, device=dev)
+        chunk_states = x.new_empty((B, -(-N // SCAN_CHUNK), D), dtype=torch.float32)
     else:
         _state(chunk_states, "chunk_states", (B, -(-N // SCAN_CHUNK), D), dev)
-    if out is None:
-        out = torch.empty(shape, dtype=dt, device=dev)
-    pitches = _pitches(shape, dt, dev, x=x, f=f, gate=gate, out=out)
+    out = _like(x) if out is None else out
+    pitches = _pitches(x, ("f", "gate", "out"), f, gate, out)
     workspace, wsb = _own_workspace(workspace, load_library().ret_scan_workspace(B, N, D, code),
                                     dev)
     _call("ret_scan", dev, _addr(x), _addr(f), _addr(gate), _addr(state_in), _addr(state_out),
@@ -549,17 +567,15 @@ def scan_step(x, f, state, form="logit", gate=None, out=None, state_out=None):
     """One token of the gated linear recurrence (ret_scan_step): x, f, gate
     [B,D]; state [B,D] float32 is updated in place, or left alone with the new
     state written to state_out.  Returns y."""
-    torch = _torch()
     if x.dim() != 2:
         raise ValueError("x must be [B,D] for a single token")
-    shape, dev, dt = x.shape, x.device, x.dtype
+    shape, dev = x.shape, x.device
     code, kind = _dtype_code(x), _code(SCAN_FORMS, form, "form")
     B, D = shape
     _state(state, "state", shape, dev)
     _state(state_out, "state_out", shape, dev)
-    if out is None:
-        out = torch.empty(shape, dtype=dt, device=dev)
-    pitches = _pitches(shape, dt, dev, x=x, f=f, gate=gate, out=out)
+    out = _like(x) if out is None else out
+    pitches = _pitches(x, ("f", "gate", "out"), f, gate, out)
     _call("ret_scan_step", dev, _addr(x), _addr(f), _addr(gate), _addr(state),
           _addr(state if state_out is None else state_out), _addr(out), pitches, B, D, kind, code)
     return out
@@ -575,20 +591,20 @@ def scan_backward(x, f, chunk_states, d_y, form="logit", gate=None, d_state_out=
     torch = _torch()
     if x.dim() != 3:
         raise ValueError("x must be [B,N,D]")
-    shape, dev, dt = x.shape, x.device, x.dtype
+    dev = x.device
     code, kind = _dtype_code(x), _code(SCAN_FORMS, form, "form")
-    B, N, D = shape
+    B, N, D = x.shape
     _state(chunk_states, "chunk_states", (B, -(-N // SCAN_CHUNK), D), dev)
     _state(d_state_out, "d_state_out", (B, D), dev)
     if gate is None and grad_gate is not None:
         raise ValueError("grad_gate given without a gate")
-    grad_x = torch.empty(shape, dtype=dt, device=dev) if grad_x is None else grad_x
-    grad_f = torch.empty(shape, dtype=dt, device=dev) if grad_f is None else grad_f
+    grad_x = _like(x) if grad_x is None else grad_x
+    grad_f = _like(x) if grad_f is None else grad_f
     if gate is not None and grad_gate is None:
-        grad_gate = torch.empty(shape, dtype=dt, device=dev)
-    pitches = _pitches(shape, dt, dev, x=x, f=f, gate=gate, d_y=d_y, grad_x=grad_x, grad_f=grad_f,
-                       grad_gate=grad_gate)
-    d_state_in = torch.empty((B, D), dtype=torch.float32, device=dev)
+        grad_gate = _like(x)
+    pitches = _pitches(x, ("f", "gate", "d_y", "grad_x", "grad_f", "grad_gate"), f, gate, d_y,
+                       grad_x, grad_f, grad_gate)
+    d_state_in = x.new_empty((B, D), dtype=torch.float32)
     workspace, wsb = _own_workspace(workspace, load_library().ret_scan_workspace(B, N, D, code),
                                     dev)
     _call("ret_scan_backward", dev, _addr(x), _addr(f), _addr(gate), _addr(chunk_states),
@@ -600,7 +616,10 @@ def scan_backward(x, f, chunk_states, d_y, form="logit", gate=None, d_state_out=
 def _head_args(y, token_major):
     if y.dim() != 4:
         raise ValueError("y must be [B,H,N,dv]")
-    _check(y, "y")
+    if not y.is_cuda:
+        raise ValueError("y must be a CUDA tensor")
+    if not y.is_contiguous():
+        raise ValueError("y must be contiguous")
     B, H, N, dv = y.shape
     return B, H, N, dv, (B, N, H, dv) if token_major else (B, H, N, dv)
 
@@ -610,7 +629,7 @@ def _head_pitch(t, name, dt, shape, dev, token_major):
     whose tokens are evenly spaced (0 for the head-major layout, which must be
     dense)."""
     if not token_major:
-        _check(t, name, dtype=dt, shape=shape, device=dev)
+        _dense(t, name, dt, shape, dev)
         return 0
     _same(t, name, dt, shape, dev)
     if t.is_contiguous():
@@ -630,13 +649,12 @@ def norm_gate(y, gate=None, norm="layer", eps=1e-5, token_major=False, out=None)
     GroupNorm of gn_eps; "rms").  With token_major, gate and o are [B,N,H,dv]
     (dense, or the gate a slice of a projection's output viewed as such);
     otherwise [B,H,N,dv].  gate None: o = z.  Returns o."""
-    torch = _torch()
     B, H, N, dv, shape = _head_args(y, token_major)
     dev, dt, code = y.device, y.dtype, _dtype_code(y)
-    kind = _code({"layer": 0, "rms": 1}, norm, "norm")
+    kind = _code(ROW_NORMS, norm, "norm")
     ldg = 0 if gate is None else _head_pitch(gate, "gate", dt, shape, dev, token_major)
     if out is None:
-        out, ldo = torch.empty(shape, dtype=dt, device=dev), 0
+        out, ldo = y.new_empty(shape) if token_major else _torch().empty_like(y), 0
     else:
         ldo = _head_pitch(out, "out", dt, shape, dev, token_major)
     _call("ret_norm_gate", dev, _addr(y), _addr(gate), _addr(out), B, H, N, dv, kind, float(eps),
@@ -648,21 +666,21 @@ def norm_gate_backward(y, gate, d_o, norm="layer", eps=1e-5, token_major=False, 
                        grad_gate=None):
     """Backward of norm_gate (ret_norm_gate_backward): returns (grad_y,
     grad_gate or None).  d_o and grad_gate are laid out like o and gate."""
-    torch = _torch()
     B, H, N, dv, shape = _head_args(y, token_major)
     dev, dt, code = y.device, y.dtype, _dtype_code(y)
-    kind = _code({"layer": 0, "rms": 1}, norm, "norm")
+    kind = _code(ROW_NORMS, norm, "norm")
     ldg = 0 if gate is None else _head_pitch(gate, "gate", dt, shape, dev, token_major)
     lddo = _head_pitch(d_o, "d_o", dt, shape, dev, token_major)
     if grad_y is None:
-        grad_y = torch.empty_like(y)
-    _check(grad_y, "grad_y", dtype=dt, shape=y.shape, device=dev)
+        grad_y = _torch().empty_like(y)
+    else:
+        _dense(grad_y, "grad_y", dt, y.shape, dev)
     ldgg = 0
     if gate is None:
         if grad_gate is not None:
             raise ValueError("grad_gate given without a gate")
     elif grad_gate is None:
-        grad_gate = torch.empty(shape, dtype=dt, device=dev)
+        grad_gate = y.new_empty(shape)
     else:
         ldgg = _head_pitch(grad_gate, "grad_gate", dt, shape, dev, token_major)
     _call("ret_norm_gate_backward", dev, _addr(y), _addr(gate), _addr(d_o), _addr(grad_y),
@@ -672,7 +690,7 @@ def norm_gate_backward(y, gate, d_o, norm="layer", eps=1e-5, token_major=False, 
 
 def _weight(w, name, d, dev):
     if w is not None:
-        _check(w, name, dtype=_torch().float32, shape=(d,), device=dev)
+        _dense(w, name, _torch().float32, (d,), dev)
 
 
 def add_norm(x, residual, w=None, w_post=None, post_norm=None, norm="rms", alpha=1.0, beta=1.0,
@@ -686,23 +704,23 @@ def add_norm(x, residual, w=None, w_post=None, post_norm=None, norm="rms", alpha
     dev, dt, code, shape = x.device, x.dtype, _dtype_code(x), x.shape
     if x.dim() < 1:
         raise ValueError("x must have a feature axis")
-    _check(x, "x")
+    _dense(x, "x", dt, shape, dev)
     d = shape[-1]
     if residual is not None:
-        _check(residual, "residual", dtype=dt, shape=shape, device=dev)
+        _dense(residual, "residual", dt, shape, dev)
     _weight(w, "w", d, dev)
     _weight(w_post, "w_post", d, dev)
     if res_out is None:
         res_out = torch.empty_like(x)
     else:
-        _check(res_out, "res_out", dtype=dt, shape=shape, device=dev)
+        _dense(res_out, "res_out", dt, shape, dev)
     if out is None:
         out = torch.empty_like(x)
     else:
-        _check(out, "out", dtype=dt, shape=shape, device=dev)
+        _dense(out, "out", dt, shape, dev)
     _call("ret_add_norm", dev, _addr(x), _addr(residual), _addr(w_post), _addr(w), _addr(res_out),
           _addr(out), x.numel() // d if d else 0, d, _code(NORMS, post_norm, "post_norm"),
-          _code({"layer": 0, "rms": 1}, norm, "norm"), float(alpha), float(beta), float(eps), code)
+          _code(ROW_NORMS, norm, "norm"), float(alpha), float(beta), float(eps), code)
     return res_out, out
 
 
@@ -717,12 +735,12 @@ def add_norm_backward(x, res_out, w, d_y, d_res_out=None, w_post=None, post_norm
     dev, dt, code, shape = res_out.device, res_out.dtype, _dtype_code(res_out), res_out.shape
     if res_out.dim() < 1:
         raise ValueError("res_out must have a feature axis")
-    _check(res_out, "res_out")
+    _dense(res_out, "res_out", dt, shape, dev)
     d = shape[-1]
     for t, name in ((x, "x"), (d_y, "d_y"), (d_res_out, "d_res_out"), (grad_x, "grad_x"),
                     (grad_residual, "grad_residual")):
         if t is not None:
-            _check(t, name, dtype=dt, shape=shape, device=dev)
+            _dense(t, name, dt, shape, dev)
     _weight(w, "w", d, dev)
     _weight(w_post, "w_post", d, dev)
     grad_x = torch.empty_like(res_out) if grad_x is None else grad_x
@@ -737,6 +755,6 @@ def add_norm_backward(x, res_out, w, d_y, d_res_out=None, w_post=None, post_norm
     _call("ret_add_norm_backward", dev, _addr(x), _addr(res_out), _addr(w_post), _addr(w),
           _addr(d_y), _addr(d_res_out), _addr(grad_x), _addr(grad_residual), _addr(grad_w),
           _addr(grad_w_post), rows, d, _code(NORMS, post_norm, "post_norm"),
-          _code({"layer": 0, "rms": 1}, norm, "norm"), float(alpha), float(beta), float(eps), code,
+          _code(ROW_NORMS, norm, "norm"), float(alpha), float(beta), float(eps), code,
           _addr(workspace), wsb)
     return grad_x, grad_residual, grad_w, grad_w_post
