@@ -349,9 +349,14 @@ RET_API int ret_rotate(const void* x, void* y, const float* theta, long long pos
  * (decays near 1 keep their precision); y is rounded once.  The result does
  * not depend on timing: the same call gives the same bits.
  * Supported: B, D >= 1, N >= 0 (N == 0 copies or zeroes state_out and writes
- * nothing else), any D; x, f, gate and y need the alignment of their element
- * type only, and run fastest where pointers and pitches are multiples of 16
- * bytes.
+ * nothing else); N and B D up to 2^31 - 4097.  x, f, gate and y need the
+ * alignment of their element type only, and run fastest where pointers and
+ * pitches are multiples of 16 bytes (other rows are read in the 16-byte
+ * granules that cover them: bytes of a row's first granule before it are read
+ * and not used).
+ * The stream must belong to the current device.  Longer sequences run as a
+ * cooperative launch, whose blocks wait for one another with a time limit
+ * (ret_device_error).
  * Outputs must not overlap inputs or one another (state_out == state_in and
  * interleaved slices of one buffer apart): RET_EINVAL.
  */

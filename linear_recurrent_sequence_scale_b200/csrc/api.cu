@@ -532,7 +532,8 @@ int check_scan(int B, int N, int D, int form, int dtype) {
   if (B < 1 || N < 0 || D < 1 || !valid_dtype(dtype)) return RET_EINVAL;
   if (form != RET_SCAN_LOGIT && form != RET_SCAN_LOG) return RET_EINVAL;
   const int64_t channels = (int64_t)B * D;
-  if (channels > INT32_MAX) return RET_EUNSUPPORTED;
+  // places up to an item past the end are computed in an int
+  if (channels > INT32_MAX - 4096 || N > INT32_MAX - 4096) return RET_EUNSUPPORTED;
   if (N > 0 && channels > ((int64_t)1 << 40) / N) return RET_EUNSUPPORTED;
   // items of 64 tokens x 32 channels are counted in an int
   const int64_t items = (int64_t)B * ((D + 31) / 32) * (((int64_t)N + 63) / 64);
@@ -691,7 +692,7 @@ int check_norm_gate(int B, int H, int N, int dv, int norm, float eps, int token_
                     long long** pitches, int n_pitches) {
   if (B < 1 || H < 1 || N < 0 || dv < 8 || dv % 8 || !valid_dtype(dtype)) return RET_EINVAL;
   if (!norm_kind(norm) || !(eps >= 0.0f) || isinf(eps)) return RET_EINVAL;
-  if (dv > 1024 || (int64_t)B * H > 65535) return RET_EUNSUPPORTED;
+  if (dv > 1024 || (int64_t)B * H > 65535 || N > INT32_MAX - 4096) return RET_EUNSUPPORTED;
   // blocks of at least eight rows are counted in an int
   if ((int64_t)B * H * (((int64_t)N + 7) / 8) > INT32_MAX) return RET_EUNSUPPORTED;
   if ((int64_t)B * H * N * dv > ((int64_t)1 << 40)) return RET_EUNSUPPORTED;

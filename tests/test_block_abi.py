@@ -64,6 +64,8 @@ def test_scan_refusals(lib):
         assert bad(**kw) == ret.RET_EINVAL, kw
     assert bad(dense=True, B=1 << 20, D=1 << 12) == ret.RET_EUNSUPPORTED
     assert bad(dense=True, N=1 << 30, D=1 << 12) == ret.RET_EUNSUPPORTED
+    assert bad(dense=True, B=1, D=1, N=(1 << 31) - 1) == ret.RET_EUNSUPPORTED
+    assert bad(dense=True, B=1, D=(1 << 31) - 1, N=1) == ret.RET_EUNSUPPORTED
     assert bad(px=(1 << 60, 64)) == ret.RET_EUNSUPPORTED
     assert bad(px=(64, 1 << 60)) == ret.RET_EUNSUPPORTED
     # short sequences of few channels need no workspace, long ones 12 bytes for each
@@ -144,6 +146,7 @@ def test_norm_gate_refusals(lib):
         assert call(**kw) == ret.RET_EINVAL, kw
     assert call(dv=2048) == ret.RET_EUNSUPPORTED
     assert call(B=1000, H=100) == ret.RET_EUNSUPPORTED
+    assert call(B=1, H=1, dv=8, N=(1 << 31) - 1) == ret.RET_EUNSUPPORTED
     assert call(N=0, y=None, g=None, o=None) == ret.RET_OK
 
 
