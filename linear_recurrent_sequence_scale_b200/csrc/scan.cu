@@ -107,7 +107,6 @@ constexpr int kWarps = 8;
 constexpr int kCompute = 32 * kWarps;
 constexpr int kPiece = 128;                // bytes of one row of an item
 constexpr uint32_t kEmpty = 0xffffffffu;   // a NaN that arithmetic never returns
-constexpr int kWindow = 4;                 // predecessors looked at together
 constexpr int kSiteForward = 801, kSiteBackward = 802;
 
 struct Plan {
@@ -117,6 +116,7 @@ struct Plan {
   int pieces;      // of all batch rows
   int tiles;       // items per piece
   int items;
+  int window;      // predecessors looked at together
   int skip_turns, skip_rest;  // from one of a block's items to its next: the grid
                               // in whole turns, and the rest of it
   // words from one turn to the next, and where a lane's begin (n channels per lane)
@@ -192,7 +192,7 @@ template <int n> __device__ __forceinline__ Vec<n> chain(Vec<n> Q, Vec<n> q) {
 
 // What enters item `tile` (> 0) of a lane's channels: `at` points at their
 // words of that item, `pitch` words from one tile to the next.
-template <int n>
+template <int kWindow, int n>
 __device__ __forceinline__ Vec<n> look_back(const Plan& p, size_t at, size_t pitch, int tile,
                                             int site) {
   Vec<n> z = all<n>(0.0f);
@@ -437,9 +437,15 @@ __device__ __forceinline__ void scout(Desk<STAGES, n>& desk, const Plan& p, int 
     if (lane == 0) sm100::mbar_arrive(&desk.full[0]);
   } else {
     for (int k = 0; !w.ends(p); ++k, w.next(p)) {
-      const Vec<n> z = w.turn > 0
-                           ? look_back<n>(p, p.words(w, n, lane), p.pitch(n), w.turn, site)
-                           : first(w.rest);
+      Vec<n> z;
+      if (w.turn == 0) {
+        z = first(w.rest);
+      } else {
+        const size_t words = p.words(w, n, lane);
+        z = p.window <= 2   ? look_back<2, n>(p, words, p.pitch(n), w.turn, site)
+            : p.window <= 4 ? look_back<4, n>(p, words, p.pitch(n), w.turn, site)
+                            : look_back<8, n>(p, words, p.pitch(n), w.turn, site);
+      }
       // the slot's previous contents (round k - 2) have been read
       if (k >= 2) sm100::mbar_wait(&desk.free[k % 2], (k / 2 - 1) % 2, site + 2);
       desk.enter[k % 2][lane] = z;
@@ -1055,6 +1061,11 @@ cudaError_t run(void (*dealt)(ScanArgs, Plan, Maps<OPERANDS, W>),
   const auto kernel = keep ? whole : dealt;
   const int units = keep ? p.pieces : p.items, grid = units < most ? units : most;
   p.skip_turns = grid / p.pieces, p.skip_rest = grid % p.pieces;
+  // More words polled delay the ones that matter, fewer make more hops of a
+  // chain: by how many predecessors are at work at once.  65536 x 4096 in bf16,
+  // 2.3 of them: 285 us looking at two, 298 at four; 65536 x 1024, 9.2: 122 at
+  // two, 107 at four, 116 at eight; 65536 x 64, 148: 68 at four, 54 at eight.
+  p.window = p.skip_turns <= 2 ? 2 : p.skip_turns <= 16 ? 4 : 8;
   Maps<OPERANDS, W> maps;
   if constexpr (W == 16)
     for (int i = 0; i < OPERANDS; ++i)
