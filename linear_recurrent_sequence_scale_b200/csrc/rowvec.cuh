@@ -41,9 +41,7 @@ template <int I> struct Int { static constexpr int value = I; };
 // At 6.5 TB/s an SM has about 31 instruction slots per lane for an element of
 // which 6 bytes move: the kernels below stay under that only with pairs and
 // with the plain hardware exponential and reciprocal.
-// A pair is one 64-bit register: held as two floats and packed at every
-// operation it would cost moves (a third of the instructions of the kernels
-// below when it was so).
+// A pair is one 64-bit register.
 template <int n> struct Vec;
 template <> struct Vec<1> {
   float a;
