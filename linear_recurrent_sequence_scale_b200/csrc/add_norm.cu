@@ -20,6 +20,8 @@
 // for rows longer than a warp's, shared memory.  y is computed from r' before
 // its rounding to the storage type, so y carries one rounding only; the
 // backward starts from the stored r'.
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "rowvec.cuh"
@@ -664,6 +666,8 @@ cudaError_t launch_add_norm(const AddNormArgs& a, cudaStream_t st) {
 
 namespace an {
 
+constexpr int kMaxDevices = 64;
+
 // Shape of the ring kernel's blocks for rows of this size.
 struct RingPlan {
   int groups = 0, stages = 0, smem = 0;  // no groups: it does not serve
@@ -692,11 +696,18 @@ cudaError_t run_ring(const AddNormArgs& a, float* ws, int* parts, cudaStream_t s
   if (!p.groups) return cudaSuccess;
   const long long want = (a.rows + p.groups - 1) / p.groups;
   const int grid = static_cast<int>(want < kRingBlocks ? want : kRingBlocks);
-  const auto kernel = a.d == G::kCH * G::kV * G::kTPR ? add_norm_ring_backward<typename G::Full>
-                                                      : add_norm_ring_backward<G>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
+  const bool exact = a.d == G::kCH * G::kV * G::kTPR;
+  const auto kernel = exact ? add_norm_ring_backward<typename G::Full> : add_norm_ring_backward<G>;
+  // the permission for the shared memory is asked for once per kernel and device
+  static std::atomic<bool> allowed[2][kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev >= kMaxDevices || !allowed[exact][dev].load()) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDevices) allowed[exact][dev].store(true);
+  }
   kernel<<<grid, p.groups * G::kTPR, p.smem, st>>>(
       a, a.grad_w ? ws : nullptr,
       a.grad_w_post ? ws + (a.grad_w ? (size_t)grid * a.d : (size_t)0) : nullptr, p.groups,
