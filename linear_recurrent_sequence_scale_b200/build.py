@@ -10,6 +10,7 @@ linked statically, so the library needs only the driver at run time.
 from __future__ import annotations
 
 import argparse
+import concurrent.futures
 import glob
 import os
 import subprocess
@@ -44,15 +45,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     hdrs = _headers()
-    objs = []
+    objs, cmds = [], []
     for src in srcs:
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
         objs.append(obj)
         if force or _stale(obj, [src] + hdrs):
-            cmd = [NVCC, *ARCH, *FLAGS, *extra_flags, "-c", src, "-o", obj]
+            cmds.append([NVCC, *ARCH, *FLAGS, *extra_flags, "-c", src, "-o", obj])
             if verbose:
-                print(" ".join(cmd), flush=True)
-            subprocess.run(cmd, check=True)
+                print(" ".join(cmds[-1]), flush=True)
+    with concurrent.futures.ThreadPoolExecutor(min(len(cmds), os.cpu_count() or 1) or 1) as pool:
+        for done in [pool.submit(subprocess.run, cmd, check=True) for cmd in cmds]:
+            done.result()
     if force or _stale(LIB, objs):
         cmd = [NVCC, *ARCH, "-shared", "-o", LIB, *objs]
         if verbose:
