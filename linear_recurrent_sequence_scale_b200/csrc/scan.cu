@@ -258,12 +258,12 @@ template <int N> __device__ __forceinline__ void cp_wait() {
 constexpr int kGranules = kPiece / 16 + 1;
 template <int W> constexpr int kRow = W == 16 ? kPiece : 16 * kGranules;  // in shared memory
 
-// TOK rows of kPiece bytes: rows past `rows` and bytes past `bytes` become zeros.
+// TOK rows of kPiece bytes: rows past `rows` and bytes past `width` become zeros.
+// The width is the piece's own (an int holds no row's bytes: D may pass 2^30).
 template <int TOK>
 __device__ __forceinline__ void copy_item(char* dst, const char* src, long long pitch, int rows,
-                                          int bytes) {
+                                          int width) {
   const uint32_t to = sm100::smem_u32(dst);
-  const int width = min(bytes, kPiece);
 #pragma unroll
   for (int k = 0; k < (TOK * kGranules + kCompute - 1) / kCompute; ++k) {
     const int i = k * kCompute + threadIdx.x;
@@ -597,15 +597,15 @@ scan_items(const ScanArgs a, const Plan p, const __grid_constant__ Maps<GATE ? 4
   const auto load = [&](int slot) {
     if (!ahead.ends(p)) {
       const int b = ahead.rest / p.blocks, d = (ahead.rest - b * p.blocks) * C;
-      const int t = ahead.turn * kTok, rows = a.N - t, bytes = (a.D - d) * (int)sizeof(T);
+      const int t = ahead.turn * kTok, rows = a.N - t, width = min(a.D - d, C) * (int)sizeof(T);
       char* s = ring + slot * R::kStage;
       copy_item<kTok>(s, (const char*)at<const T>(a.f, b, t, d), a.f.token * sizeof(T), rows,
-                         bytes);
+                         width);
       copy_item<kTok>(s + kX, (const char*)at<const T>(a.x, b, t, d), a.x.token * sizeof(T),
-                         rows, bytes);
+                         rows, width);
       if constexpr (GATE)
         copy_item<kTok>(s + kGate, (const char*)at<const T>(a.gate, b, t, d),
-                           a.gate.token * sizeof(T), rows, bytes);
+                           a.gate.token * sizeof(T), rows, width);
       ahead.next(p);
     }
     cp_commit();
@@ -759,17 +759,17 @@ scan_items_backward(const ScanArgs a, const Plan p,
     if (!ahead.ends(p)) {
       const int b = ahead.rest / p.blocks, d = (ahead.rest - b * p.blocks) * C;
       const int t = (p.tiles - 1 - ahead.turn) * kTok;
-      const int rows = a.N - t, bytes = (a.D - d) * (int)sizeof(T);
+      const int rows = a.N - t, width = min(a.D - d, C) * (int)sizeof(T);
       char* s = ring + slot * R::kStage;
       copy_item<kTok>(s, (const char*)at<const T>(a.f, b, t, d), a.f.token * sizeof(T), rows,
-                         bytes);
+                         width);
       copy_item<kTok>(s + kX, (const char*)at<const T>(a.x, b, t, d), a.x.token * sizeof(T),
-                         rows, bytes);
+                         rows, width);
       copy_item<kTok>(s + kDy, (const char*)at<const T>(a.d_y, b, t, d),
-                         a.d_y.token * sizeof(T), rows, bytes);
+                         a.d_y.token * sizeof(T), rows, width);
       if constexpr (GATE)
         copy_item<kTok>(s + kGate, (const char*)at<const T>(a.gate, b, t, d),
-                           a.gate.token * sizeof(T), rows, bytes);
+                           a.gate.token * sizeof(T), rows, width);
       ahead.next(p);
     }
     cp_commit();
