@@ -345,9 +345,10 @@ RET_API int ret_rotate(const void* x, void* y, const float* theta, long long pos
  *   workspace  : at least ret_scan_workspace() bytes, 16-byte aligned;
  *                contents on entry do not matter.  Calls that may overlap on
  *                the GPU need a workspace each.
- * The recurrence runs in float32 whatever dtype is, with 1 - a taken directly
- * (decays near 1 keep their precision); y is rounded once.  The result does
- * not depend on timing: the same call gives the same bits.
+ * The recurrence runs in float32 whatever dtype is, a decay above 1/2 by 1 - a
+ * and one below it by a (both keep their relative precision, and so do the
+ * gradients that they scale); y is rounded once.  The result does not depend
+ * on timing: the same call gives the same bits.
  * Supported: B, D >= 1, N >= 0 (N == 0 copies or zeroes state_out and writes
  * nothing else); N and B D up to 2^31 - 4097.  x, f, gate and y need the
  * alignment of their element type only, and run fastest where pointers and

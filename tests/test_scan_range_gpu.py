@@ -1,8 +1,12 @@
 """The gated linear recurrence at the ends of its stated range: rows of more than
-2^31 bytes."""
+2^31 bytes, and decays close to 0."""
+import numpy as np
 import pytest
 
+import oracle
+from block_bounds import U, store, within
 from test_block_gpu import no_device_error, ret, torch  # noqa: F401 (fixtures)
+from test_block_gpu import Draws, host
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +39,129 @@ def test_scan_of_a_very_wide_row(torch, ret, dt, D):
     for i, w in zip(spots(D), want):
         got = ret.scan_backward(part(x, i), part(f, i), part(cs, i), part(d_y, i))
         assert all(torch.equal(part(g, i), v) for g, v in zip(grads, got) if v is not None)
+
+
+# --- decays close to 0 ---------------------------------------------------------------
+#
+# Bounds relative to the sums of absolute values; u = 2^-24 is one float32 rounding.
+#   a decay a    (10 + 2.4 |f|) u of itself: the exponential as in block_bounds, an
+#                addition, a quotient (2 units of 2u), a product, and two roundings
+#                in a product of decays; LOG, where a span's decay is that of the sum
+#                of its f in four parts of at most eight: 9 |f| u more
+#   1 - a        (12 + 2.4 |f|) u of itself
+#   a step of h  three roundings (the input, a z + input in two), and for each span
+#                of at least 16 tokens the two of a fold and three of a product of
+#                two spans: at most 4 u of m_t = a m_(t-1) + |u_t| a step; the flow
+#                out of a span, a sum of 16 products, 16 u of itself at most, of which
+#                its 16 steps have 4 u each
+# and 2^-125 of the largest value, below which a product of decays is no normal number.
+
+def decay_error(f, form):
+    return (10 + (2.4 if form == "logit" else 11.4) * np.abs(f)) * U
+
+
+def forward_bound(x, f, form, state_in):
+    """(h, bound of h, m)."""
+    a, c = oracle.scan_gates(f, form)
+    _, h = oracle.scan(x, f, form, None, state_in)
+    r = decay_error(f, form)
+    u = np.abs(c * x) if form == "logit" else np.abs(x)
+    e_u = u * ((12 + 2.4 * np.abs(f)) * U if form == "logit" else 0.0)
+    e, m = np.zeros_like(h), np.zeros_like(h)
+    m_t = np.zeros(h.shape[::2]) if state_in is None else np.abs(state_in)
+    top, e_t = 1.0 + m_t, np.zeros_like(m_t)
+    for t in range(h.shape[1]):
+        e_t = a[:, t] * e_t + r[:, t] * a[:, t] * m_t + e_u[:, t]
+        m_t = a[:, t] * m_t + u[:, t]
+        top = np.maximum(top, m_t)
+        e_t = e_t + 4 * U * m_t
+        e[:, t], m[:, t] = e_t + 2.0 ** -125 * top, m_t
+    return h, e, m
+
+
+def backward_bound(x, f, form, d_y, state_in, d_state_out):
+    """Bounds of (dx, df, d_state_in), before their rounding to the storage type."""
+    a, c = oracle.scan_gates(f, form)
+    h, e_h, _ = forward_bound(x, f, form, state_in)
+    before, e_before = oracle.entering(h, state_in), oracle.entering(e_h)
+    r, r_c = decay_error(f, form), (12 + 2.4 * np.abs(f)) * U
+    m_t = np.abs(d_state_out)
+    e_t, top = np.zeros_like(m_t), 1.0 + m_t
+    b_x, b_f = np.zeros_like(h), np.zeros_like(h)
+    for t in range(h.shape[1] - 1, -1, -1):
+        m_g = m_t + np.abs(d_y[:, t])
+        e_g = e_t + U * m_g
+        top = np.maximum(top, m_g)
+        m_t = a[:, t] * m_g
+        e_t = a[:, t] * e_g + (r[:, t] + 4 * U) * m_t + 2.0 ** -125 * top
+        if form == "logit":
+            lever = np.abs(before[:, t] - x[:, t])
+            e_lever = e_before[:, t] + U * lever
+            b_x[:, t] = c[:, t] * (e_g + (r_c[:, t] + U) * m_g)
+            b_f[:, t] = c[:, t] * (e_lever * m_t + lever * (e_t + (r_c[:, t] + 2 * U) * m_t))
+        else:
+            b_x[:, t] = e_g
+            b_f[:, t] = e_before[:, t] * m_t + np.abs(before[:, t]) * (e_t + U * m_t)
+    return b_x, b_f, e_t
+
+
+def strong(d, kind, B, N, D):
+    """f: strongly forgetting gates, a mixture of them with long memories, or a
+    steady decay of 0.9 (whose products are small though no decay is)."""
+    f = -d.rng.uniform(8.0, 20.0, (B, N, D))
+    if kind == "mixed":
+        keep = d.rng.random((B, N, D)) < 0.7
+        f = np.where(keep, d.rng.uniform(-3.0, 9.0, (B, N, D)), f)
+    return f
+
+
+STRONG = [("f32", 1, 1, 33), ("f32", 2, 40, 64), ("f32", 1, 300, 31), ("bf16", 2, 300, 72),
+          ("f32", 1, 700, 32), ("bf16", 1, 3000, 64), ("f32", 1, 3000, 33)]
+
+
+def strong_inputs(torch, c, form, kind, seed):
+    dt, B, N, D = c
+    d = Draws(torch, dt, seed)
+    if kind == "steady":
+        f = np.full((B, N, D), np.log(9.0) if form == "logit" else np.log(0.9))
+        x = np.where(np.arange(N) % 600 < 3, 1.0, 0.0)[None, :, None] * np.ones((B, N, D))
+    else:
+        f = strong(d, kind, B, N, D)
+        if form == "log":
+            f = -np.logaddexp(0.0, -f)
+        x = 1e-3 * d.rng.random((B, N, D))
+        x[:, ::50] = 1e3                       # large states before small inputs
+    return d, d.put(x), d.put(f), d.put(1e3 * d.rng.random((B, D)), torch.float32)
+
+
+@pytest.mark.parametrize("kind", ["strong", "mixed", "steady"])
+@pytest.mark.parametrize("form", ["logit", "log"])
+@pytest.mark.parametrize("c", STRONG, ids=lambda c: "-".join(map(str, c)))
+def test_scan_with_decays_close_to_0(torch, ret, c, form, kind):
+    """Every input is positive, so the bounds are relative to each value itself."""
+    d, x, f, s0 = strong_inputs(torch, c, form, kind, 31)
+    y, s, cs = ret.scan(x, f, form=form, state_in=s0, return_state=True, return_chunk_states=True)
+    h, e, m = forward_bound(host(x), host(f), form, host(s0))
+    assert (m == h).all()
+    assert within(host(y), h, e + store(c[0]) * np.abs(h)) <= 1
+    assert within(host(s), h[:, -1], e[:, -1]) <= 1
+    B, N, D = c[1:]
+    d_y, d_s = d.put(d.rng.random((B, N, D)) + 0.1), d.put(d.rng.random((B, D)), torch.float32)
+    got = ret.scan_backward(x, f, cs, d_y, form=form, d_state_out=d_s)
+    want = oracle.scan_backward(host(x), host(f), form, host(d_y), None, host(s0), host(d_s))
+    b_x, b_f, b_s = backward_bound(host(x), host(f), form, host(d_y), host(s0), host(d_s))
+    assert within(host(got[0]), want[0], b_x + store(c[0]) * np.abs(want[0])) <= 1
+    assert within(host(got[1]), want[1], b_f + store(c[0]) * np.abs(want[1])) <= 1
+    assert within(host(got[3]), want[3], b_s) <= 1
+
+
+@pytest.mark.parametrize("dt,B,D", [("f32", 3, 64), ("f32", 2, 33), ("bf16", 5, 1000)])
+@pytest.mark.parametrize("form", ["logit", "log"])
+def test_step_with_decays_close_to_0(torch, ret, form, dt, B, D):
+    d, x, f, s0 = strong_inputs(torch, (dt, B, 2, D), form, "strong", 32)
+    x, f = x[:, 1], f[:, 1]
+    s = s0.clone()
+    y = ret.scan_step(x, f, s, form=form)
+    h, e, _ = forward_bound(host(x)[:, None], host(f)[:, None], form, host(s0))
+    assert within(host(s), h[:, 0], e[:, 0]) <= 1
+    assert within(host(y), h[:, 0], e[:, 0] + store(dt) * np.abs(h[:, 0])) <= 1
