@@ -326,8 +326,11 @@ RET_API int ret_rotate(const void* x, void* y, const float* theta, long long pos
  *     RET_SCAN_LOGIT   a = sigmoid(f),  h_t = a_t h_(t-1) + (1 - a_t) x_t
  *     RET_SCAN_LOG     a = exp(f),      h_t = a_t h_(t-1) + x_t
  * y_t = h_t, or swish(gate_t) h_t when a gate is given.  f = -inf is a decay
- * of 0: nothing of the state before that token counts (a document that starts
- * inside a packed row).  RET_SCAN_LOG expects f <= 0; larger values grow.
+ * of 0: nothing of a finite state before that token counts (a document that
+ * starts inside a packed row).  A state that is infinite or NaN stays so (0
+ * times it is NaN) to the end of its channel's batch row, and a gradient that
+ * is stays so to the row's beginning.  RET_SCAN_LOG expects f <= 0; larger
+ * values grow.
  *   x, f, gate : [B][N][D] of type dtype; gate may be NULL.
  *   y          : [B][N][D] of type dtype.
  *   pitches    : HOST array {x, f, gate, y} x {batch, token}: elements from

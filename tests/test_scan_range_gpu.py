@@ -1,5 +1,5 @@
 """The gated linear recurrence at the ends of its stated range: rows of more than
-2^31 bytes, and decays close to 0."""
+2^31 bytes, decays close to 0, and values that are not finite."""
 import numpy as np
 import pytest
 
@@ -56,8 +56,12 @@ def test_scan_of_a_very_wide_row(torch, ret, dt, D):
 #                its 16 steps have 4 u each
 # and 2^-125 of the largest value, below which a product of decays is no normal number.
 
+def size(f):
+    return np.where(np.isfinite(f), np.abs(f), 0.0)       # a decay of 0 is exact
+
+
 def decay_error(f, form):
-    return (10 + (2.4 if form == "logit" else 11.4) * np.abs(f)) * U
+    return (10 + (2.4 if form == "logit" else 11.4) * size(f)) * U
 
 
 def forward_bound(x, f, form, state_in):
@@ -66,7 +70,7 @@ def forward_bound(x, f, form, state_in):
     _, h = oracle.scan(x, f, form, None, state_in)
     r = decay_error(f, form)
     u = np.abs(c * x) if form == "logit" else np.abs(x)
-    e_u = u * ((12 + 2.4 * np.abs(f)) * U if form == "logit" else 0.0)
+    e_u = u * ((12 + 2.4 * size(f)) * U if form == "logit" else 0.0)
     e, m = np.zeros_like(h), np.zeros_like(h)
     m_t = np.zeros(h.shape[::2]) if state_in is None else np.abs(state_in)
     top, e_t = 1.0 + m_t, np.zeros_like(m_t)
@@ -84,7 +88,7 @@ def backward_bound(x, f, form, d_y, state_in, d_state_out):
     a, c = oracle.scan_gates(f, form)
     h, e_h, _ = forward_bound(x, f, form, state_in)
     before, e_before = oracle.entering(h, state_in), oracle.entering(e_h)
-    r, r_c = decay_error(f, form), (12 + 2.4 * np.abs(f)) * U
+    r, r_c = decay_error(f, form), (12 + 2.4 * size(f)) * U
     m_t = np.abs(d_state_out)
     e_t, top = np.zeros_like(m_t), 1.0 + m_t
     b_x, b_f = np.zeros_like(h), np.zeros_like(h)
@@ -93,16 +97,17 @@ def backward_bound(x, f, form, d_y, state_in, d_state_out):
         e_g = e_t + U * m_g
         top = np.maximum(top, m_g)
         m_t = a[:, t] * m_g
-        e_t = a[:, t] * e_g + (r[:, t] + 4 * U) * m_t + 2.0 ** -125 * top
+        e_t = a[:, t] * e_g + (r[:, t] + 4 * U) * m_t
+        e_g, e_f = e_g + 2.0 ** -125 * top, e_t + 2.0 ** -125 * top
         if form == "logit":
             lever = np.abs(before[:, t] - x[:, t])
             e_lever = e_before[:, t] + U * lever
             b_x[:, t] = c[:, t] * (e_g + (r_c[:, t] + U) * m_g)
-            b_f[:, t] = c[:, t] * (e_lever * m_t + lever * (e_t + (r_c[:, t] + 2 * U) * m_t))
+            b_f[:, t] = c[:, t] * (e_lever * m_t + lever * (e_f + (r_c[:, t] + 2 * U) * m_t))
         else:
             b_x[:, t] = e_g
-            b_f[:, t] = e_before[:, t] * m_t + np.abs(before[:, t]) * (e_t + U * m_t)
-    return b_x, b_f, e_t
+            b_f[:, t] = e_before[:, t] * m_t + np.abs(before[:, t]) * (e_f + U * m_t)
+    return b_x, b_f, e_f
 
 
 def strong(d, kind, B, N, D):
@@ -165,3 +170,42 @@ def test_step_with_decays_close_to_0(torch, ret, form, dt, B, D):
     h, e, _ = forward_bound(host(x)[:, None], host(f)[:, None], form, host(s0))
     assert within(host(s), h[:, 0], e[:, 0]) <= 1
     assert within(host(y), h[:, 0], e[:, 0] + store(dt) * np.abs(h[:, 0])) <= 1
+
+
+# --- values that are not finite --------------------------------------------------------
+
+@pytest.mark.parametrize("N", [200, 3000])
+@pytest.mark.parametrize("value", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("form", ["logit", "log"])
+def test_scan_of_documents_with_a_value_that_is_not_finite(torch, ret, form, value, N):
+    """Two documents in a row, such an input (or gradient) in the first (the last):
+    a decay of 0 drops every finite state exactly, and that value stays in its own
+    channel and batch row, on its own side of where it is."""
+    B, D, at, reset = 2, 40, 20, 90
+    d = Draws(torch, "f32", 33)
+    x, f = d.normal(B, N, D), -d.normal(B, N, D).abs()
+    f[:, reset] = -np.inf
+    x[:, :reset] *= 1e30                         # far larger states before the reset
+    clean = ret.scan(x, f, form=form)
+    alone = ret.scan(x[:, reset:], f[:, reset:], form=form)
+    h, e, m = forward_bound(host(x[:, reset:]), host(f[:, reset:]), form, None)
+    for y in (clean[:, reset:], alone):          # nothing of the first document is left
+        assert within(host(y), h, e) <= 1
+    x[1, at, 3] = value
+    y = ret.scan(x, f, form=form)
+    rest = torch.ones_like(y, dtype=torch.bool)
+    rest[1, at:, 3] = False
+    assert torch.equal(y[rest], clean[rest])
+    assert not torch.isfinite(y[~rest]).any()
+    x[1, at, 3] = 0.0
+    _, cs = ret.scan(x, f, form=form, return_chunk_states=True)
+    d_y = d.normal(B, N, D)
+    clean = ret.scan_backward(x, f, cs, d_y, form=form)
+    d_y[0, N - 10, 5] = value
+    got = ret.scan_backward(x, f, cs, d_y, form=form)
+    rest = torch.ones_like(x, dtype=torch.bool)
+    rest[0, :N - 9, 5] = False
+    assert torch.equal(got[0][rest], clean[0][rest])
+    assert torch.equal(got[1][rest], clean[1][rest])
+    assert not torch.isfinite(got[0][~rest]).any()
+    assert not torch.isfinite(got[3][0, 5])
