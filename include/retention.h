@@ -330,7 +330,8 @@ RET_API int ret_rotate(const void* x, void* y, const float* theta, long long pos
  * starts inside a packed row).  A state that is infinite or NaN stays so (0
  * times it is NaN) to the end of its channel's batch row, and a gradient that
  * is stays so to the row's beginning.  RET_SCAN_LOG expects f <= 0; larger
- * values grow.
+ * values grow, as far as the decays of no 256 tokens in a row multiply to more
+ * than float32 holds (a zero state stays zero beyond that, too).
  *   x, f, gate : [B][N][D] of type dtype; gate may be NULL.
  *   y          : [B][N][D] of type dtype.
  *   pitches    : HOST array {x, f, gate, y} x {batch, token}: elements from

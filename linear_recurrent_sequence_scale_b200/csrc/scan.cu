@@ -237,15 +237,29 @@ template <int n> __device__ __forceinline__ Vec<n> fold(Vec<n> z, Vec<n> M, Vec<
   return decayed(z, M, near_one(M), Z);
 }
 
+// No more than the largest float32 (a NaN stays one): a product of decays above
+// 1 that no float32 holds leaves a zero state zero then, and ends at a decay of 0.
+template <int FORM, int n> __device__ __forceinline__ Vec<n> bounded(Vec<n> p) {
+  if constexpr (FORM == RET_SCAN_LOGIT) {
+    return p;
+  } else {
+    float v[n];
+#pragma unroll
+    for (int i = 0; i < n; ++i)
+      asm("min.NaN.f32 %0, %1, 0f7f7fffff;" : "=f"(v[i]) : "f"(p[i]));
+    return vec(v);
+  }
+}
+
 // A product of decays, P, and its difference from 1, Q: each is exact where
 // the other is not, and the product is held by Q from P = 5/8 on (of LOGIT's
 // decays none at or below 1/2 is in it then).
-template <int n> struct Product {
+template <int FORM, int n> struct Product {
   Vec<n> P = all<n>(1.0f), Q = all<n>(0.0f);
   __device__ __forceinline__ void take(Vec<n> m) {  // one more span
     const Vec<n> c = near_one(m);
     Q = fma(less_one(m, c), P, Q);
-    P = mul(P, add(m, c));
+    P = bounded<FORM>(mul(P, add(m, c)));
   }
   __device__ __forceinline__ Vec<n> held() const {
     float m[n];
@@ -256,24 +270,24 @@ template <int n> struct Product {
 };
 
 // The product of a warp's tokens.  LOG: e to the sum of their f, in four parts.
-template <int FORM, int n> struct Tokens : Product<n> {
-  using Product<n>::P;
-  using Product<n>::Q;
+template <int FORM, int n> struct Tokens : Product<FORM, n> {
+  using Product<FORM, n>::P;
+  using Product<FORM, n>::Q;
   Vec<n> part[4] = {all<n>(0.0f), all<n>(0.0f), all<n>(0.0f), all<n>(0.0f)};
   __device__ __forceinline__ void take(int j, Vec<n> f, const Decay<n>& a) {
     if constexpr (FORM == RET_SCAN_LOGIT)
       Q = fma(a.q, P, Q);
     else
       part[j % 4] = add(part[j % 4], f);
-    P = mul(P, a.a);  // (LOG: for the backward's flow alone)
+    P = bounded<FORM>(mul(P, a.a));  // (LOG: for the backward's flow alone)
   }
   __device__ __forceinline__ Vec<n> held() const {
-    if constexpr (FORM == RET_SCAN_LOGIT) return Product<n>::held();
+    if constexpr (FORM == RET_SCAN_LOGIT) return Product<FORM, n>::held();
     const Vec<n> f = add(add(part[0], part[1]), add(part[2], part[3]));
     float below[n];  // a sum of 0 is held as a difference from 1, too
 #pragma unroll
     for (int i = 0; i < n; ++i) below[i] = f[i] == 0.0f ? -0.0f : f[i];
-    return decay<FORM>(vec(below)).m;
+    return bounded<FORM>(decay<FORM>(vec(below)).m);
   }
 };
 
@@ -743,7 +757,7 @@ scan_items(const ScanArgs a, const Plan p, const __grid_constant__ Maps<GATE ? 4
     compute_sync();
 
     // 2. the span of the warps before, and of the item
-    Product<n> behind;
+    Product<FORM, n> behind;
     V Zb = all<n>(0.0f);
 #pragma unroll
     for (int v = 0; v < kWarps - 1; ++v) {
@@ -941,7 +955,7 @@ scan_items_backward(const ScanArgs a, const Plan p,
     compute_sync();
 
     // 2. the span of the warps behind, and of the item
-    Product<n> behind;
+    Product<FORM, n> behind;
     V Eb = all<n>(0.0f);
 #pragma unroll
     for (int v = kWarps - 1; v > 0; --v) {

@@ -1,5 +1,6 @@
 """The gated linear recurrence at the ends of its stated range: rows of more than
-2^31 bytes, decays close to 0, and values that are not finite."""
+2^31 bytes, decays close to 0, values that are not finite, and
+decays above 1."""
 import numpy as np
 import pytest
 
@@ -209,3 +210,40 @@ def test_scan_of_documents_with_a_value_that_is_not_finite(torch, ret, form, val
     assert torch.equal(got[1][rest], clean[1][rest])
     assert not torch.isfinite(got[0][~rest]).any()
     assert not torch.isfinite(got[3][0, 5])
+
+
+# --- growth ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dt,N,D", [("f32", 700, 40), ("bf16", 3000, 72), ("f32", 3000, 33)])
+@pytest.mark.parametrize("grow", [0.5, 6.0])
+def test_scan_of_growing_decays_over_a_zero_state(torch, ret, dt, N, D, grow):
+    """f > 0 whose products over a span, or over a few tokens, no float32 holds: a
+    zero state stays zero there, a decay of 0 ends the growth, and so do the
+    gradients behind a last such token."""
+    B, quiet = 2, N - 200
+    d = Draws(torch, dt, 34)
+    x, f = d.normal(B, N, D), -d.normal(B, N, D).abs()
+    x[:, :quiet], f[:, :quiet] = 0.0, grow
+    y, s, cs = ret.scan(x, f, form="log", return_state=True, return_chunk_states=True)
+    h, e, _ = forward_bound(host(x[:, quiet:]), host(f[:, quiet:]), "log", None)
+    assert not y[:, :quiet].any() and not cs[:, :quiet // ret.SCAN_CHUNK].any()
+    assert within(host(y[:, quiet:]), h, e + store(dt) * np.abs(h) + 1e-37) <= 1
+    assert within(host(s), h[:, -1], e[:, -1]) <= 1
+    # growth between two decays of 0, in both directions
+    x, f, d_y = d.normal(B, N, D), -d.normal(B, N, D).abs(), d.normal(B, N, D)
+    quiet = np.zeros(N, bool)
+    for i, k in ((20, 60), (300, 560)):
+        quiet[i:k] = True
+        x[:, i:k], f[:, i:k], d_y[:, i:k] = 0.0, grow, 0.0
+        f[:, i], f[:, k] = -np.inf, -np.inf
+    y, cs = ret.scan(x, f, form="log", return_chunk_states=True)
+    h, e, _ = forward_bound(host(x), host(f), "log", None)
+    assert within(host(y), h, e + store(dt) * np.abs(h) + 1e-37) <= 1 and not host(y)[:, quiet].any()
+    zero = np.zeros((B, D))
+    got = ret.scan_backward(x, f, cs, d_y, form="log")
+    want = oracle.scan_backward(host(x), host(f), "log", host(d_y))
+    b_x, b_f, b_s = backward_bound(host(x), host(f), "log", host(d_y), None, zero)
+    assert within(host(got[0]), want[0], b_x + store(dt) * np.abs(want[0]) + 1e-37) <= 1
+    assert within(host(got[1]), want[1], b_f + store(dt) * np.abs(want[1]) + 1e-37) <= 1
+    assert within(host(got[3]), want[3], b_s + 1e-37) <= 1
+    assert not host(got[0])[:, quiet].any()
