@@ -504,6 +504,15 @@ RET_API int ret_device_error(void);
  */
 RET_API int ret_selftest_bounded_wait(int limit_ms, void* stream);
 
+/*
+ * The same for the recurrence: one block of it works on the second of two
+ * items while no block works on the first, so its look-back runs out after
+ * limit_ms and the block ends with a site code of 801 .. 811.  The workspace
+ * (16-byte aligned, at least 256 KB) holds the call's rows.
+ */
+RET_API int ret_selftest_scan_wait(int limit_ms, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
 /* Library version string (static storage). */
 RET_API const char* ret_version(void);
 

@@ -67,6 +67,7 @@ SIGNATURES = {
     "ret_version": (ctypes.c_char_p, []),
     "ret_device_error": (_I, []),
     "ret_selftest_bounded_wait": (_I, [_I, _P]),
+    "ret_selftest_scan_wait": (_I, [_I, _P, _S, _P]),
 }
 
 _lib = None

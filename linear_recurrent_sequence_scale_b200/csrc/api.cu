@@ -87,6 +87,14 @@ int ret_selftest_bounded_wait(int limit_ms, void* stream) {
       ret::launch_bounded_wait_selftest(limit_ms, static_cast<cudaStream_t>(stream)));
 }
 
+int ret_selftest_scan_wait(int limit_ms, void* workspace, size_t workspace_bytes, void* stream) {
+  if (limit_ms < 1 || limit_ms > 10000) return RET_EINVAL;
+  if (!workspace || workspace_bytes < ret::kSelftestBytes) return RET_EWORKSPACE;
+  if (!aligned16(workspace)) return RET_EINVAL;
+  return cuda_status(ret::launch_scan_wait_selftest(limit_ms, workspace,
+                                                    static_cast<cudaStream_t>(stream)));
+}
+
 int ret_parallel_gated(const void* q, const void* k, const void* v, const float* gammas,
                        const void* gate, void* o, int B, int H, int N, int dk, int dv, int dtype,
                        float gn_eps, void* stream) {

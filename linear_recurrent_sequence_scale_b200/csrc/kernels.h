@@ -70,6 +70,9 @@ struct ScanArgs {
 };
 size_t scan_workspace_bytes(int B, int N, int D, int dtype);
 int scan_device_error();
+// Self-test of its waits: published words, then f, x and y.
+constexpr size_t kSelftestRows = 1024, kSelftestBytes = 256 * 1024;
+cudaError_t launch_scan_wait_selftest(int limit_ms, void* ws, cudaStream_t st);
 cudaError_t launch_scan(const ScanArgs& a, cudaStream_t st);
 cudaError_t launch_scan_backward(const ScanArgs& a, cudaStream_t st);
 cudaError_t launch_scan_step(const ScanArgs& a, cudaStream_t st);

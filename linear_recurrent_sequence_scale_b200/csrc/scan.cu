@@ -169,6 +169,8 @@ struct Plan {
   int window;      // predecessors looked at together
   int skip_turns, skip_rest;  // from one of a block's items to its next: the grid
                               // in whole turns, and the rest of it
+  int first;       // turn of the first block's first item (not 0 in the self-test)
+  uint64_t limit;  // of every wait, ns
   // words from one turn to the next, and where a lane's begin (n channels per lane)
   __device__ __forceinline__ size_t pitch(int n) const { return (size_t)pieces * 32 * n; }
   template <typename Item>
@@ -330,7 +332,7 @@ __device__ __forceinline__ Vec<n> look_back(const Plan& p, size_t at, size_t pit
       if (t0 == 0) t0 = now;
       // out of time, or another wait was: the whole warp gives up together
       if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&g_device_error) != 0 ||
-                                      now - t0 > sm100::kWaitLimitNs)) {
+                                      now - t0 > p.limit)) {
         sm100::record_error(site);
         return all<n>(__uint_as_float(0x7fffffffu));
       }
@@ -478,7 +480,7 @@ template <bool WHOLE> struct Walk {
   int turn;  // place in the order that state flows: 0 has no predecessor
   int rest;  // batch row and piece of its channels in one
   __device__ __forceinline__ Walk(const Plan& p)
-      : turn(WHOLE ? 0 : blockIdx.x / p.pieces),
+      : turn(WHOLE ? 0 : p.first + blockIdx.x / p.pieces),
         rest(WHOLE ? blockIdx.x : blockIdx.x % p.pieces) {}
   __device__ __forceinline__ void next(const Plan& p) {
     if constexpr (WHOLE) {
@@ -542,7 +544,7 @@ __device__ __forceinline__ void scout(Desk<STAGES, n>& desk, const Plan& p, int 
                             : look_back<8, n>(p, words, p.pitch(n), w.turn, site);
       }
       // the slot's previous contents (round k - 2) have been read
-      if (k >= 2) sm100::mbar_wait(&desk.free[k % 2], (k / 2 - 1) % 2, site + 2);
+      if (k >= 2) sm100::mbar_wait(&desk.free[k % 2], (k / 2 - 1) % 2, site + 2, p.limit);
       desk.enter[k % 2][lane] = z;
       __syncwarp();
       if (lane == 0) sm100::mbar_arrive(&desk.full[k % 2]);
@@ -554,13 +556,14 @@ __device__ __forceinline__ void scout(Desk<STAGES, n>& desk, const Plan& p, int 
 // keeps whole pieces it was put there in round k - 1, on the far side of this
 // round's barrier (only round 0 has it from the scout).
 template <bool WHOLE, int STAGES, int n>
-__device__ __forceinline__ Vec<n> entering(Desk<STAGES, n>& desk, int k, int site) {
+__device__ __forceinline__ Vec<n> entering(Desk<STAGES, n>& desk, const Plan& p, int k,
+                                           int site) {
   const int lane = threadIdx.x % 32;
   if constexpr (WHOLE) {
-    if (k == 0) sm100::mbar_wait(&desk.full[0], 0, site + 4);
+    if (k == 0) sm100::mbar_wait(&desk.full[0], 0, site + 4, p.limit);
     return desk.enter[k % 2][lane];
   } else {
-    sm100::mbar_wait(&desk.full[k % 2], (k / 2) % 2, site + 4);
+    sm100::mbar_wait(&desk.full[k % 2], (k / 2) % 2, site + 4, p.limit);
     const Vec<n> z = desk.enter[k % 2][lane];
     __syncwarp();
     if (lane == 0) sm100::mbar_arrive(&desk.free[k % 2]);
@@ -613,7 +616,10 @@ __device__ __forceinline__ void mover(Desk<STAGES, n>& desk, char* ring, const P
 #pragma unroll
     for (int s = 0; s < STAGES; ++s, ++k) {
       if (!ok || w.ends(p)) break;
-      ok = sm100::mbar_wait(&desk.done[s], (k / STAGES) % 2, site + 6);
+      // The computing warps say done after a wait that gave up as well: the slot is
+      // touched again only once its own load has landed.
+      ok = sm100::mbar_wait(&desk.done[s], (k / STAGES) % 2, site + 6, p.limit) &&
+           sm100::mbar_wait(&desk.loaded[s], (k / STAGES) % 2, site + 6, p.limit);
       if (!ok) break;
       const int b = w.rest / p.blocks, d = (w.rest - b * p.blocks) * C;
       const int t = tile(w.turn) * TOK;
@@ -713,7 +719,7 @@ scan_items(const ScanArgs a, const Plan p, const __grid_constant__ Maps<GATE ? 4
     const int b = w.rest / p.blocks, d = (w.rest - b * p.blocks) * C + lane * n, left = a.D - d;
     const int t0 = w.turn * kTok + warp * S, mine = min(S, a.N - t0);
     if constexpr (kTma) {
-      sm100::mbar_wait(&desk.loaded[slot], phase, kSiteForward + 8);
+      sm100::mbar_wait(&desk.loaded[slot], phase, kSiteForward + 8, p.limit);
     } else {
       cp_wait<ST - 2>();
       compute_sync();  // the item is here, and the previous one's slot is free
@@ -773,7 +779,7 @@ scan_items(const ScanArgs a, const Plan p, const __grid_constant__ Maps<GATE ? 4
       M = behind.held();
       if (publish && !WHOLE) st_words(p.span + 2 * p.words(w, n, lane), M, Z);
     }
-    V z = entering<WHOLE>(desk, k, kSiteForward);
+    V z = entering<WHOLE>(desk, p, k, kSiteForward);
     if (warp == kWarps - 1) {
       if constexpr (WHOLE)
         desk.enter[(k + 1) % 2][lane] = publish ? fold(z, M, Z) : first(w.rest + gridDim.x);
@@ -900,7 +906,7 @@ scan_items_backward(const ScanArgs a, const Plan p,
                  : nullptr,
         left);
     if constexpr (kTma) {
-      sm100::mbar_wait(&desk.loaded[slot], phase, kSiteBackward + 8);
+      sm100::mbar_wait(&desk.loaded[slot], phase, kSiteBackward + 8, p.limit);
     } else {
       cp_wait<ST - 2>();
       compute_sync();
@@ -990,7 +996,7 @@ scan_items_backward(const ScanArgs a, const Plan p,
     }
 
     // 3. the gradients, backwards
-    V flow = entering<WHOLE>(desk, k, kSiteBackward);
+    V flow = entering<WHOLE>(desk, p, k, kSiteBackward);
     if (warp == 0) {
       if constexpr (WHOLE)
         desk.enter[(k + 1) % 2][lane] = publish ? fold(flow, M, E) : first(w.rest + gridDim.x);
@@ -1088,6 +1094,7 @@ Plan plan(const ScanArgs& a, int tok) {
   p.tiles = cdiv(a.N, tok);
   p.pieces = a.B * p.blocks;
   p.items = p.pieces * p.tiles;
+  p.limit = sm100::kWaitLimitNs;
   if (p.tiles > 1) {
     const size_t n = words(a.B, a.D, a.dtype, p.tiles);
     p.span = static_cast<float*>(a.workspace);
@@ -1245,9 +1252,39 @@ cudaError_t backward(const ScanArgs& a, cudaStream_t st) {
   }
 }
 
+// The second of two items whose predecessor no block works on.
+cudaError_t lone_item(void* ws, uint64_t limit, cudaStream_t st) {
+  constexpr int D = 32, N = 2 * kTokForward;
+  char* rows = static_cast<char*>(ws) + kSelftestRows;
+  ScanArgs a = {};
+  Operand* const ops[] = {&a.f, &a.x, &a.y};
+  for (int i = 0; i < 3; ++i) *ops[i] = {rows + i * sizeof(float) * N * D, N * D, D};
+  a.B = 1, a.N = N, a.D = D, a.form = RET_SCAN_LOG, a.dtype = RET_F32, a.workspace = ws;
+  const auto kernel = scan_items<float, RET_SCAN_LOG, false, 16, false>;
+  constexpr int smem = Ring<2, 2, kTokForward, 16>::kBytes;
+  Plan p = plan(a, kTokForward);
+  p.skip_turns = 1, p.window = 2, p.first = 1, p.limit = limit;
+  Maps<3, 16> maps;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  for (int i = 0; i < 3 && e == cudaSuccess; ++i)
+    e = map_operand(&maps.m[i], *ops[i], a, kTokForward);
+  if (e == cudaSuccess) e = cudaMemsetAsync(ws, 0xff, kSelftestRows, st);
+  if (e == cudaSuccess) e = cudaMemsetAsync(rows, 0, kSelftestBytes - kSelftestRows, st);
+  if (e != cudaSuccess) return e;
+  kernel<<<1, kBlockOf<16>, smem, st>>>(a, p, maps);
+  return cudaPeekAtLastError();
+}
+
 }  // namespace scan
 
 int scan_device_error() { return read_clear_device_error(); }
+
+cudaError_t launch_scan_wait_selftest(int limit_ms, void* ws, cudaStream_t st) {
+  static_assert(kSelftestRows >= 12 * 2 * 32 &&
+                    kSelftestBytes >= kSelftestRows + 3 * sizeof(float) * 2 * scan::kTokForward * 32,
+                "two items of 32 float32 channels");
+  return scan::lone_item(ws, static_cast<uint64_t>(limit_ms) * 1000000ull, st);
+}
 
 // For either direction and any alignment: as many items as the shortest make.
 size_t scan_workspace_bytes(int B, int N, int D, int dtype) {
