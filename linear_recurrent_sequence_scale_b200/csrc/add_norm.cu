@@ -457,6 +457,7 @@ add_norm_ring_backward(AddNormArgs a, float* part_w, float* part_post, int group
   R acc_w, acc_post;
 #pragma unroll
   for (int i = 0; i < R::P; ++i) acc_w.p[i] = acc_post.p[i] = all<2>(0.0f);
+  int fetched = 0;  // rows, by the group's first thread
   // Row n into stage s: by the group's first thread, as bulk copies; rows that
   // are not 16-byte aligned by all of its threads, granule by granule.
   const auto fetch = [&](long long n, int s) {
@@ -485,6 +486,7 @@ add_norm_ring_backward(AddNormArgs a, float* part_w, float* part_post, int group
     const auto load = [&](const void* p, uint32_t place) {
       sm100::bulk_load(to + place, static_cast<const T*>(p) + n * a.d, row, &full[group][s]);
     };
+    ++fetched;
     sm100::mbar_arrive_expect_tx(&full[group][s], stage);
     load(a.res_out, 0);
     load(a.d_y, row);
@@ -495,9 +497,10 @@ add_norm_ring_backward(AddNormArgs a, float* part_w, float* part_post, int group
     for (int s = 0; s < stages; ++s) fetch(first + group + s * step, s);
     const float inv_d = 1.0f / a.d;
     int s = 0, phase = 0;
+    bool ok = true;  // every row waited for has landed
     for (long long n = first + group; n < a.rows; n += step) {
       if constexpr (kWhole) {
-        sm100::mbar_wait(&full[group][s], phase, kSiteRing + 1);
+        ok = sm100::mbar_wait(&full[group][s], phase, kSiteRing + 1) && ok;
       } else {
         asm volatile("cp.async.wait_group %0;" ::"n"(kGranuleStages - 1) : "memory");
         B::sync(group);
@@ -550,7 +553,7 @@ add_norm_ring_backward(AddNormArgs a, float* part_w, float* part_post, int group
       // and through the one after the block
       if (need_x) load(h, stage - row, a.x);
       B::sync(group);  // the stage has been read
-      fetch(n + stages * step, s);
+      if (ok) fetch(n + stages * step, s);  // after a wait gave up a copy may be under way
       if (post) B::apply(h, mx, layer_post, lane, nv);
       if (part_post) acc_post.add_product(d, h);
       if (a.grad_x) {
@@ -560,13 +563,10 @@ add_norm_ring_backward(AddNormArgs a, float* part_w, float* part_post, int group
       }
       if (++s == stages) s = 0, phase ^= 1;
     }
-    // where some wait gave up, the copies still under way end before the block does
-    if (kWhole && lane == 0 && sm100::failed())
-      for (int i = 0; i < stages; ++i) {
-        const long long mine = a.rows - first - group;  // rows of the group: ceil(mine / step)
-        const long long rows = mine > 0 ? (mine + step - 1) / step : 0;
-        if (rows > i) sm100::mbar_drain(&full[group][i], ((rows - 1 - i) / stages) % 2);
-      }
+    // and they end before the block does
+    if (kWhole && lane == 0 && !ok)
+      for (int i = 0; i < stages; ++i)
+        if (fetched > i) sm100::mbar_drain(&full[group][i], ((fetched - 1 - i) / stages) % 2);
   }
   if constexpr (!kWhole) asm volatile("cp.async.wait_group 0;" ::: "memory");
   // the groups' sums, through the place of their rings, in the groups' order

@@ -123,10 +123,6 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   }
 }
 
-// Whether some wait of this unit has given up.
-__device__ __forceinline__ bool failed() {
-  return *reinterpret_cast<volatile int*>(&g_device_error) != 0;
-}
 // For copies under way after some wait gave up: their phase, within the limit,
 // whatever the error flag says.
 __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
