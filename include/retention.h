@@ -349,8 +349,8 @@ RET_API int ret_rotate(const void* x, void* y, const float* theta, long long pos
  *   workspace  : at least ret_scan_workspace() bytes, 16-byte aligned;
  *                contents on entry do not matter.  Calls that may overlap on
  *                the GPU need a workspace each.
- * The recurrence runs in float32 whatever dtype is, a decay above 1/2 by 1 - a
- * and one below it by a (both keep their relative precision, and so do the
+ * The recurrence runs in float32 whatever dtype is, a decay near 1 by 1 - a
+ * and one near 0 by a (both keep their relative precision, and so do the
  * gradients that they scale); y is rounded once.  The result does not depend
  * on timing: the same call gives the same bits.
  * Supported: B, D >= 1, N >= 0 (N == 0 copies or zeroes state_out and writes
@@ -360,8 +360,8 @@ RET_API int ret_rotate(const void* x, void* y, const float* theta, long long pos
  * granules that cover them: bytes of a row's first granule before it are read
  * and not used).
  * The stream must belong to the current device.  Longer sequences run as a
- * cooperative launch, whose blocks wait for one another with a time limit
- * (ret_device_error).
+ * cooperative launch, whose blocks wait for one another with a time limit of
+ * 2 s for each wait; ret_device_error tells whether one ran out.
  * Outputs must not overlap inputs or one another (state_out == state_in and
  * interleaved slices of one buffer apart): RET_EINVAL.
  */
@@ -488,10 +488,13 @@ RET_API const char* ret_status_string(int status);
 RET_API int ret_last_cuda_error(void);
 
 /*
- * Reads and clears the flag the tensor-core kernels set when one of their
- * bounded waits on an mbarrier ran out (a protocol failure that would
- * otherwise hang the GPU): 0 if none, otherwise the code of the wait site, -1
- * if the flag could not be read.  Synchronous with respect to the device.
+ * Reads and clears the flag the kernels set when one of their bounded waits
+ * ran out (a protocol failure that would otherwise hang the GPU): 0 if none,
+ * otherwise the code of the wait site, -1 if the flag could not be read.
+ * Synchronous with respect to the device.  What the call that waited has
+ * written is not valid, although it returned RET_OK; and until the flag is
+ * read, later calls of the same kernels give up their waits early, so theirs
+ * may not be either.
  */
 RET_API int ret_device_error(void);
 

@@ -101,7 +101,8 @@ def status_string(status: int) -> str:
 
 
 def device_error() -> int:
-    """Read and clear the tensor-core kernels' timed-out-wait flag (0 = none)."""
+    """Read and clear the kernels' timed-out-wait flag (0 = none).  What was written
+    since the last reading is not valid where this returns another code."""
     return int(load_library().ret_device_error())
 
 
@@ -536,6 +537,8 @@ def scan(x, f, form="logit", gate=None, state_in=None, state_out=None, return_st
     state_in, state_out: [B,D] float32 before the first and after the last
     token; state_out may be state_in.  chunk_states:
     [B, ceil(N / SCAN_CHUNK), D] float32, kept for scan_backward.
+    Long sequences are dealt over blocks that wait for one another, each wait
+    with a limit: device_error() tells whether one ran out.
     Returns y, or the tuple (y[, state][, chunk_states]) with what
     return_state / state_out and return_chunk_states / chunk_states ask for.
     """
