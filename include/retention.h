@@ -423,8 +423,8 @@ RET_API int ret_scan_backward(const void* x, const void* f, const void* gate,
  *          a slice of a projection and o feeds the next one.  gate may be
  *          NULL (norm only).  o may equal y or gate where their layouts and
  *          pitches agree; outputs must not overlap inputs otherwise.
- * Supported: dv a multiple of 8 in [8, 1024]; all pointers 16-byte aligned;
- * N == 0 writes nothing.
+ * Supported: dv a multiple of 8 in [8, 1024], B H up to 65535; all pointers
+ * 16-byte aligned; N == 0 writes nothing.
  *
  * Backward: with d_o the gradient of o (laid out like o, pitch lddo), writes
  * grad_y ([B][H][N][dv]) and, with a gate, grad_gate (laid out like gate,

@@ -652,7 +652,8 @@ def norm_gate(y, gate=None, norm="layer", eps=1e-5, token_major=False, out=None)
     o = swish(gate) * z, z each row of y [B,H,N,dv] normalised ("layer": the
     GroupNorm of gn_eps; "rms").  With token_major, gate and o are [B,N,H,dv]
     (dense, or the gate a slice of a projection's output viewed as such);
-    otherwise [B,H,N,dv].  gate None: o = z.  Returns o."""
+    otherwise [B,H,N,dv].  gate None: o = z.  dv: a multiple of 8 up to 1024;
+    B H up to 65535.  Returns o."""
     B, H, N, dv, shape = _head_args(y, token_major)
     dev, dt, code = y.device, y.dtype, _dtype_code(y)
     kind = _code(ROW_NORMS, norm, "norm")
