@@ -61,7 +61,6 @@ template <typename T, int V, int CH, int TPR, bool FULL = false> struct Geo {
   static constexpr int kV = V, kCH = CH, kTPR = TPR;
   static constexpr int kThreads = TPR < 64 ? 128 : TPR;  // several short rows per block
   static constexpr int kRows = kThreads / TPR;
-  
 };
 
 template <typename G>
@@ -181,9 +180,9 @@ __device__ __forceinline__ void put_partials(const AddNormArgs& a, int lane, int
   }
 }
 
-// Persistent over rows, loads straight into registers: rows that do not split
-// into 16-byte pieces, short ones (several per block), and those too long for
-// the ring below.
+// Persistent over rows, loads straight into registers: rows under 512 bytes
+// (several per block), and those that the ring below cannot hold, wider than
+// 16 KB (8192 elements where they do not split into 16-byte pieces).
 template <typename G>
 __global__ void __launch_bounds__(G::kThreads)
 add_norm_rows_backward(AddNormArgs a, float* part_w, float* part_post) {
@@ -493,81 +492,79 @@ add_norm_ring_backward(AddNormArgs a, float* part_w, float* part_post, int group
     if (a.d_res_out) load(a.d_res_out, 2 * row);
     if (need_x) load(a.x, stage - row);
   };
-  {
-    for (int s = 0; s < stages; ++s) fetch(first + group + s * step, s);
-    const float inv_d = 1.0f / a.d;
-    int s = 0, phase = 0;
-    bool ok = true;  // every row waited for has landed
-    for (long long n = first + group; n < a.rows; n += step) {
-      if constexpr (kWhole) {
-        ok = sm100::mbar_wait(&full[group][s], phase, kSiteRing + 1) && ok;
-      } else {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kGranuleStages - 1) : "memory");
-        B::sync(group);
-      }
-      const char* here = ring + (group * stages + s) * stage;
-      const long long at = n * a.d;
-      const auto load = [&](R& part, uint32_t place, const void* p) {
-        const uint32_t off =
-            kWhole ? 0 : (uint32_t) reinterpret_cast<uintptr_t>(static_cast<const T*>(p) + at) & 15;
-        part.load(reinterpret_cast<const T*>(here + place + off), lane, nv);
-      };
-      R h, d;
-      // both norms' moments
-      float2 mine_x = make_float2(0.0f, 0.0f);
-      if (post) {
-        load(d, stage - row, a.x);
-        mine_x = B::own(d, layer_post, lane, nv);
-      }
-      load(h, 0, a.res_out);
-      const float2 mine_h = B::own(h, layer, lane, nv);
-      const Vec<2> m2 = warp_sum(two(mine_h.y, mine_x.y));
-      if (lane % 32 == 0)
-        moments[group][lane / 32] = make_float4(mine_h.x, m2[0], mine_x.x, m2[1]);
+  for (int s = 0; s < stages; ++s) fetch(first + group + s * step, s);
+  const float inv_d = 1.0f / a.d;
+  int s = 0, phase = 0;
+  bool ok = true;  // every row waited for has landed
+  for (long long n = first + group; n < a.rows; n += step) {
+    if constexpr (kWhole) {
+      ok = sm100::mbar_wait(&full[group][s], phase, kSiteRing + 1) && ok;
+    } else {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kGranuleStages - 1) : "memory");
       B::sync(group);
-      const Moments mh = B::join(
-          [&](int i) { return make_float2(moments[group][i].x, moments[group][i].y); }, layer,
-          a.eps, inv_d, nv);
-      Moments mx = {0.0f, 1.0f};
-      if (post)
-        mx = B::join([&](int i) { return make_float2(moments[group][i].z, moments[group][i].w); },
-                     layer_post, a.eps, inv_d, nv);
-      if (B::W == 1) __syncwarp();  // read before the next row's are written
-      // through the norm before the next block
-      B::apply(h, mh, layer, lane, nv);
-      load(d, row, a.d_y);
-      if (part_w) acc_w.add_product(d, h);
-      if (a.w) B::scale(d, w, lane, nv);
-      B::back(d, h, mh.r, layer, inv_d, slots[group][0], group, lane, nv);
-      if (a.d_res_out) {
-        load(h, 2 * row, a.d_res_out);
-#pragma unroll
-        for (int i = 0; i < R::P; ++i) d.p[i] = add(d.p[i], h.p[i]);
-      }
-      if (a.grad_residual) {
-        h = d;
-        h.times(a.alpha);
-        h.store(static_cast<T*>(a.grad_residual) + at, lane, nv);
-      }
-      d.times(a.beta);
-      // and through the one after the block
-      if (need_x) load(h, stage - row, a.x);
-      B::sync(group);  // the stage has been read
-      if (ok) fetch(n + stages * step, s);  // after a wait gave up a copy may be under way
-      if (post) B::apply(h, mx, layer_post, lane, nv);
-      if (part_post) acc_post.add_product(d, h);
-      if (a.grad_x) {
-        if (a.w_post) B::scale(d, w_post, lane, nv);
-        if (post) B::back(d, h, mx.r, layer_post, inv_d, slots[group][1], group, lane, nv);
-        d.store(static_cast<T*>(a.grad_x) + at, lane, nv);
-      }
-      if (++s == stages) s = 0, phase ^= 1;
     }
-    // and they end before the block does
-    if (kWhole && lane == 0 && !ok)
-      for (int i = 0; i < stages; ++i)
-        if (fetched > i) sm100::mbar_drain(&full[group][i], ((fetched - 1 - i) / stages) % 2);
+    const char* here = ring + (group * stages + s) * stage;
+    const long long at = n * a.d;
+    const auto load = [&](R& part, uint32_t place, const void* p) {
+      const uint32_t off =
+          kWhole ? 0 : (uint32_t) reinterpret_cast<uintptr_t>(static_cast<const T*>(p) + at) & 15;
+      part.load(reinterpret_cast<const T*>(here + place + off), lane, nv);
+    };
+    R h, d;
+    // both norms' moments
+    float2 mine_x = make_float2(0.0f, 0.0f);
+    if (post) {
+      load(d, stage - row, a.x);
+      mine_x = B::own(d, layer_post, lane, nv);
+    }
+    load(h, 0, a.res_out);
+    const float2 mine_h = B::own(h, layer, lane, nv);
+    const Vec<2> m2 = warp_sum(two(mine_h.y, mine_x.y));
+    if (lane % 32 == 0)
+      moments[group][lane / 32] = make_float4(mine_h.x, m2[0], mine_x.x, m2[1]);
+    B::sync(group);
+    const Moments mh = B::join(
+        [&](int i) { return make_float2(moments[group][i].x, moments[group][i].y); }, layer,
+        a.eps, inv_d, nv);
+    Moments mx = {0.0f, 1.0f};
+    if (post)
+      mx = B::join([&](int i) { return make_float2(moments[group][i].z, moments[group][i].w); },
+                   layer_post, a.eps, inv_d, nv);
+    if (B::W == 1) __syncwarp();  // read before the next row's are written
+    // through the norm before the next block
+    B::apply(h, mh, layer, lane, nv);
+    load(d, row, a.d_y);
+    if (part_w) acc_w.add_product(d, h);
+    if (a.w) B::scale(d, w, lane, nv);
+    B::back(d, h, mh.r, layer, inv_d, slots[group][0], group, lane, nv);
+    if (a.d_res_out) {
+      load(h, 2 * row, a.d_res_out);
+#pragma unroll
+      for (int i = 0; i < R::P; ++i) d.p[i] = add(d.p[i], h.p[i]);
+    }
+    if (a.grad_residual) {
+      h = d;
+      h.times(a.alpha);
+      h.store(static_cast<T*>(a.grad_residual) + at, lane, nv);
+    }
+    d.times(a.beta);
+    // and through the one after the block
+    if (need_x) load(h, stage - row, a.x);
+    B::sync(group);  // the stage has been read
+    if (ok) fetch(n + stages * step, s);  // after a wait gave up a copy may be under way
+    if (post) B::apply(h, mx, layer_post, lane, nv);
+    if (part_post) acc_post.add_product(d, h);
+    if (a.grad_x) {
+      if (a.w_post) B::scale(d, w_post, lane, nv);
+      if (post) B::back(d, h, mx.r, layer_post, inv_d, slots[group][1], group, lane, nv);
+      d.store(static_cast<T*>(a.grad_x) + at, lane, nv);
+    }
+    if (++s == stages) s = 0, phase ^= 1;
   }
+  // and they end before the block does
+  if (kWhole && lane == 0 && !ok)
+    for (int i = 0; i < stages; ++i)
+      if (fetched > i) sm100::mbar_drain(&full[group][i], ((fetched - 1 - i) / stages) % 2);
   if constexpr (!kWhole) asm volatile("cp.async.wait_group 0;" ::: "memory");
   // the groups' sums, through the place of their rings, in the groups' order
   float* sums = reinterpret_cast<float*>(ring);

@@ -137,7 +137,8 @@ __device__ __forceinline__ T* at(const Operand& o, long long b, long long t, lon
 // back over the previous items of the same channels until it meets one whose
 // end is published, and folds forward from there over the published spans.
 // So every element crosses HBM once, and neither few channels nor long
-// sequences leave SMs idle.  (With the look-back done by one of the eight
+// sequences leave SMs idle: the single-pass prefix scan with decoupled
+// look-back (Merrill and Garland, 2016).  (With the look-back done by one of the eight
 // warps between 2 and 3, the others waited for it 60% of the time: 556 us
 // instead of 401 us for 65536 x 4096 in bf16.)
 //
@@ -865,9 +866,11 @@ scan_items_backward(const ScanArgs a, const Plan p,
       const auto tile = [&](int turn) { return p.tiles - 1 - turn; };
       if (lane == 0) {
         if constexpr (GATE)
-          mover<WHOLE, R, IN, 3, kTok>(desk, ring, p, maps.m, maps.m + IN, {0, 1, 3}, kSiteBackward, tile);
+          mover<WHOLE, R, IN, 3, kTok>(desk, ring, p, maps.m, maps.m + IN, {0, 1, 3},
+                                       kSiteBackward, tile);
         else
-          mover<WHOLE, R, IN, 2, kTok>(desk, ring, p, maps.m, maps.m + IN, {0, 1}, kSiteBackward, tile);
+          mover<WHOLE, R, IN, 2, kTok>(desk, ring, p, maps.m, maps.m + IN, {0, 1},
+                                       kSiteBackward, tile);
       }
       return;
     }
@@ -1075,10 +1078,6 @@ cudaError_t dispatch(int dtype, int form, bool gate, Fn fn) {
   return dtype == RET_BF16 ? with_form(Type<__nv_bfloat16>()) : with_form(Type<float>());
 }
 
-}  // namespace scan
-
-namespace scan {
-
 int channels_per_piece(int dtype) { return kPiece / (dtype == RET_BF16 ? 2 : 4); }
 
 // Words of one kind (end states; half of the spans) that `tiles` items per
@@ -1142,10 +1141,14 @@ cudaError_t map_operand(Mapped* m, const Operand& o, const ScanArgs& a, int tok)
 
 // Whether blocks keep whole pieces, of `most` that run at once: then neither
 // the workspace nor a cooperative launch is needed, but a block's rounds follow
-// one another, and are as many as the fullest block's.  Worth it up to ten
-// rounds (4 us less for 256 x 256 in float32), and where few are wasted (8 x
-// 2048 x 2048 gated: 16 rounds instead of 13.8, 64 us either way); 2 x 8192 x
-// 4096 takes 111 us in whole pieces, 93 dealt.
+// one another, and are as many as the fullest block's.  Dealing the items
+// instead costs as much as two to four rounds (of the backward's shorter ones,
+// four to seven): in bf16, pieces x tokens, 148 x 4096 gated, 16 rounds either
+// way, 61 us in whole pieces and 66 dealt; 128 x 8192, 32 rounds or 27.7, 79 us
+// both ways; 160 x 2048, 16 or 8.6, 43 and 33.  And it costs a call 2 us on the
+// host, as much as a few rounds: 32 x 1024 in float32, 4 rounds or 0.9, 17 and
+// 20 us a call, 64 x 2048, 8 or 3.5, 18 and 20; in bf16, whose rounds are
+// longer, 32 x 2048, 8 or 1.7, 23 and 20.
 constexpr int kFewRounds = 10;
 bool keeps_whole(const Plan& p, int most) {
   const int64_t rounds = (int64_t)p.tiles * ((p.pieces + most - 1) / most);
@@ -1197,8 +1200,8 @@ cudaError_t run(void (*dealt)(ScanArgs, Plan, Maps<OPERANDS, W>),
   p.skip_turns = grid / p.pieces, p.skip_rest = grid % p.pieces;
   // More words polled delay the ones that matter, fewer make more hops of a
   // chain: by how many predecessors are at work at once.  65536 x 4096 in bf16,
-  // 2.3 of them: 285 us looking at two, 298 at four; 65536 x 1024, 9.2: 122 at
-  // two, 107 at four, 116 at eight; 65536 x 64, 148: 68 at four, 54 at eight.
+  // 2.3 of them: 280 us looking at two, 298 at four; 65536 x 1024, 9.2: 155 at
+  // two, 107 at four, 112 at eight; 65536 x 64, 148: 81 at four, 58 at eight.
   p.window = p.skip_turns <= 2 ? 2 : p.skip_turns <= 16 ? 4 : 8;
   Maps<OPERANDS, W> maps;
   if constexpr (W == 16)
@@ -1280,8 +1283,8 @@ cudaError_t lone_item(void* ws, uint64_t limit, cudaStream_t st) {
 int scan_device_error() { return read_clear_device_error(); }
 
 cudaError_t launch_scan_wait_selftest(int limit_ms, void* ws, cudaStream_t st) {
-  static_assert(kSelftestRows >= 12 * 2 * 32 &&
-                    kSelftestBytes >= kSelftestRows + 3 * sizeof(float) * 2 * scan::kTokForward * 32,
+  constexpr size_t operand = sizeof(float) * 2 * scan::kTokForward * 32;
+  static_assert(kSelftestRows >= 12 * 2 * 32 && kSelftestBytes >= kSelftestRows + 3 * operand,
                 "two items of 32 float32 channels");
   return scan::lone_item(ws, static_cast<uint64_t>(limit_ms) * 1000000ull, st);
 }
