@@ -250,7 +250,8 @@ constexpr int kMaxStages = 4;
 // The same serves rows that are not 16-byte aligned: they come as the granules
 // that cover them (the bytes before a row lie in its own first 16 bytes of
 // memory; none behind it is read), and threads take single elements.  16384 x
-// 4095 in bf16: 824 us with single elements from HBM, 399 so.
+// 4095 in bf16, an RMS and a layer norm: 824 us with single elements from HBM,
+// 399 so.
 constexpr int kGranuleStages = 2;
 constexpr int kRingWarps = 12;  // three on each scheduler: 168 registers a thread
 constexpr int kRingBytes = 225 * 1024;  // beside 1 KB of barriers and sums
