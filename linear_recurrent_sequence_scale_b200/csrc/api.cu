@@ -563,9 +563,13 @@ int check_operand(const ret::Operand& o, int B, int N, int D, int dtype) {
 }
 
 // Operand k of a call: its pitches in elements from the host array, or dense.
+// A single token has no pitch to the next: whatever is given for it (a span of
+// one token of a longer sequence, say) does not reach the kernels, which
+// address rows behind the last one by it and count on its alignment.
 ret::Operand operand(const void* p, const long long* pitches, int k, int N, int D) {
   ret::Operand o = {const_cast<void*>(p), (long long)N * D, D};
-  if (pitches) o.batch = pitches[2 * k], o.token = pitches[2 * k + 1];
+  if (pitches) o.batch = pitches[2 * k];
+  if (pitches && N > 1) o.token = pitches[2 * k + 1];
   return o;
 }
 

@@ -1,5 +1,5 @@
 """The gated linear recurrence at the ends of its stated range: rows of more than
-2^31 bytes, decays close to 0, values that are not finite, and
+2^31 bytes, spans of a few tokens at any alignment, decays close to 0, values that are not finite, and
 decays above 1."""
 import numpy as np
 import pytest
@@ -40,6 +40,40 @@ def test_scan_of_a_very_wide_row(torch, ret, dt, D):
     for i, w in zip(spots(D), want):
         got = ret.scan_backward(part(x, i), part(f, i), part(cs, i), part(d_y, i))
         assert all(torch.equal(part(g, i), v) for g, v in zip(grads, got) if v is not None)
+
+
+# --- spans of a few tokens of a longer sequence -----------------------------------------
+
+@pytest.mark.parametrize("n", [1, 2, 33])
+@pytest.mark.parametrize("B", [1, 3])
+@pytest.mark.parametrize("dt,D,room", [("bf16", 64, 67), ("bf16", 64, 66), ("bf16", 33, 40),
+                                       ("bf16", 130, 135), ("f32", 64, 67), ("f32", 31, 32)])
+def test_scan_of_a_short_span(torch, ret, dt, D, room, B, n):
+    """Rows of `room` elements, odd ones among them, from every start: what dense
+    copies give within the bounds of both."""
+    d = Draws(torch, dt, 35)
+    N = 40
+    flat = [d.put(d.rng.standard_normal(B * N * room + 8)) for _ in range(4)]
+    for first in (0, 1, 2):
+        x, f, g, d_y = (t[first:first + B * N * room].view(B, N, room)[..., :D] for t in flat)
+        for at in (0, 1, N - n):
+            xs, fs, gs, ds = (t[:, at:at + n] for t in (x, f, g, d_y))
+            out = torch.full((B, n + 2, room), 7.0, device="cuda", dtype=x.dtype)
+            y, cs = ret.scan(xs, fs, gate=gs, out=out[:, 1:n + 1, :D], return_chunk_states=True)
+            h, e, _ = forward_bound(host(xs), host(fs), "logit", None)
+            gh = host(gs)
+            sw = gh / (1 + np.exp(-gh))
+            b = np.abs(sw) * e + ((24 + 2.4 * np.abs(gh)) * U + store(dt)) * np.abs(h * sw)
+            assert within(host(y), h * sw, 1.01 * b + 1e-37) <= 1
+            assert (out[:, 0] == 7).all() and (out[:, n + 1] == 7).all()
+            assert (out[:, :, D:] == 7).all()
+            got = ret.scan_backward(xs, fs, cs, ds)
+            want = oracle.scan_backward(host(xs), host(fs), "logit", host(ds))
+            zero = np.zeros((B, D))
+            b_x, b_f, b_s = backward_bound(host(xs), host(fs), "logit", host(ds), None, zero)
+            assert within(host(got[0]), want[0], b_x + store(dt) * np.abs(want[0]) + 1e-37) <= 1
+            assert within(host(got[1]), want[1], b_f + store(dt) * np.abs(want[1]) + 1e-37) <= 1
+            assert within(host(got[3]), want[3], b_s + 1e-37) <= 1
 
 
 # --- decays close to 0 ---------------------------------------------------------------
