@@ -61,14 +61,14 @@ template <int FORM, int n> __device__ __forceinline__ Decay<n> decay(Vec<n> f) {
   const Vec<n> e = exp2v(mul(f, all<n>(kLog2e)));
   float pick[n], c[n];
   if constexpr (FORM == RET_SCAN_LOGIT) {
-    r.q = add(rcpv(fma(e, all<n>(-1.0f), all<n>(-1.0f))), all<n>(-kLeast));
+    r.q = rcpv(fma(e, all<n>(-1.0f), all<n>(-1.0f)));
 #pragma unroll
     for (int i = 0; i < n; ++i) {
       const bool near = f[i] > 0.0f;
       pick[i] = near ? 1.0f : -e[i];
       c[i] = near ? 1.0f : 0.0f;
     }
-    r.m = mul(r.q, vec(pick));
+    r.m = mul(add(r.q, all<n>(-kLeast)), vec(pick));
     r.a = add(r.m, vec(c));
   } else {
     Vec<n> s = fma(f, all<n>(1.0f / 720.0f), all<n>(1.0f / 120.0f));
@@ -85,9 +85,9 @@ template <int FORM, int n> __device__ __forceinline__ Decay<n> decay(Vec<n> f) {
   }
   return r;
 }
-// q from m and c.
+// q from m and c; 0 again where the decay is exactly 1.
 template <int n> __device__ __forceinline__ Vec<n> less_one(Vec<n> m, Vec<n> c) {
-  return add(m, add(c, all<n>(-1.0f)));
+  return add(fma(c, all<n>(kLeast), m), add(c, all<n>(-1.0f)));
 }
 // a z, and a z + more.
 template <int n> __device__ __forceinline__ Vec<n> decayed(Vec<n> z, Vec<n> m, Vec<n> c) {

@@ -246,6 +246,34 @@ def test_scan_of_documents_with_a_value_that_is_not_finite(torch, ret, form, val
     assert not torch.isfinite(got[3][0, 5])
 
 
+@pytest.mark.parametrize("dt,N,D", [("f32", 300, 40), ("f32", 3000, 33), ("bf16", 300, 72),
+                                    ("bf16", 3000, 66), ("bf16", 700, 65)])
+@pytest.mark.parametrize("gate", [False, True])
+def test_scan_takes_nothing_where_the_gate_is_open(torch, ret, dt, N, D, gate):
+    """f = inf in the logit form: the state stays as it is whatever x is, and neither
+    x nor f has a gradient; the decay is exactly 1 for what comes after."""
+    B = 2
+    d = Draws(torch, dt, 36)
+    x, f, g = d.normal(B, N, D), d.normal(B, N, D), d.normal(B, N, D) if gate else None
+    f[:, 50:] = np.inf
+    x[:, 50:] = 1e38
+    # (not bit by bit: the end of a span is rounded otherwise than its tokens' states)
+    y, s = ret.scan(x, f, gate=g, return_state=True)
+    h, e, _ = forward_bound(host(x), host(f), "logit", None)
+    gh = host(g) if gate else np.zeros((B, N, D))
+    sw = gh / (1 + np.exp(-gh)) if gate else 1.0
+    b = np.abs(sw) * e + ((24 + 2.4 * np.abs(gh)) * U + store(dt)) * np.abs(h * sw)
+    assert within(host(y), h * sw, 1.01 * b + 1e-37) <= 1
+    assert within(host(s), h[:, -1], e[:, -1]) <= 1
+    _, cs = ret.scan(x, f, return_chunk_states=True)
+    d_y = d.normal(B, N, D)
+    got = ret.scan_backward(x, f, cs, d_y, gate=g)
+    assert not got[0][:, 50:].any() and not got[1][:, 50:].any()
+    step = s.clone()
+    ret.scan_step(x[:, 60], f[:, 60], step)
+    assert torch.equal(step, s)
+
+
 # --- growth ---------------------------------------------------------------------------
 
 @pytest.mark.parametrize("dt,N,D", [("f32", 700, 40), ("bf16", 3000, 72), ("f32", 3000, 33)])
