@@ -358,7 +358,7 @@ template <int N> __device__ __forceinline__ void cp_wait() {
 // 16 bytes of memory), those behind the piece or the row's end are not.
 // Copied 4 bytes at a time, 8 x 2048 x 2046 in bf16 took 122 us gated and 222
 // backward, and with a bf16's alignment (2047), through registers, 427 and
-// 557; in granules 102 and 185, 118 and 181.
+// 557; in granules 103 and 189, 117 and 186.
 constexpr int kGranules = kPiece / 16 + 1;
 template <int W> constexpr int kRow = W == 16 ? kPiece : 16 * kGranules;  // in shared memory
 
